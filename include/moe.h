@@ -379,6 +379,135 @@ moe_status moe_backward_profiled(const moe_shape* s, moe_dtype dt, const uint16_
                                  int dw_fp32, void* ws, void* const* events /* host */,
                                  void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Ragged grouped products, int8 products and block norms: the pieces around and inside an expert
+ * layer that is not the SwiGLU layer above (other activations, one matrix per expert, int8
+ * weights), with plain 16-bit tensors. They take the schedule (offsets, perm) of moe_permute.
+ *
+ * Types and sizes. moe_gemm_shape: R routed rows, K and N the expert matrix's sizes, E experts;
+ * R >= 0, E <= 1024, K and N any number from 1 (not only multiples of a tile). Row pitches (ld_*)
+ * are in elements and at least the row's width. A buffer without elements (R or T = 0) may be
+ * NULL. Offsets live on the device and are not read by the host; the kernels clamp them to
+ * ascending values in [0, R], and source rows to [0, src_rows).
+ * Beyond the sizes stated at a call: MOE_EUNSUPPORTED for R > 2^30, K or N > 2^20, E > 1024, or
+ * more than 2^30 tiles of 32 rows x 128 columns.
+ * ------------------------------------------------------------------------------------------- */
+typedef enum { MOE_ELT_BF16 = 0, MOE_ELT_FP16 = 1, MOE_ELT_F32 = 2 } moe_elt;
+
+typedef struct {
+  int32_t R; /* routed rows (dense product: tokens), >= 0 */
+  int32_t K; /* rows of an expert's matrix (input width), >= 1 */
+  int32_t N; /* columns of an expert's matrix (output width), >= 1 */
+  int32_t E; /* experts, 1 .. 1024 */
+} moe_gemm_shape;
+
+/* ---------------------------------------------------------------------------------------------
+ * moe_grouped_gemm: out[r] = rows[src(r)] W[e] for offsets[e] <= r < offsets[e+1].
+ * moe_grouped_gemm_dgrad: dx[r] = dy[src(r)] W[e]^T (the gradient of the rows; with weights stored
+ *   [E][N][K], "y = x W^T", it is the forward product of the shape with K and N exchanged).
+ * moe_grouped_gemm_wgrad: dw[e] = sum over the expert's rows r of rows[src(r)]^T dy[r].
+ *
+ * dt: MOE_ELT_BF16 or MOE_ELT_FP16 for rows, dy and w; outputs dt or MOE_ELT_F32. Sums are
+ * float32, with one rounding at the store.
+ * w [E][K][N] in every call. rows [..][K] with pitch ld_rows, out [R][N] with pitch ld_out, dy
+ * [R][N] (pitch ld_dy), dx [R][K] (pitch ld_dx), dw [E][K][N] dense.
+ * row_src NULL: src(r) = r, and src_rows (the rows behind `rows`) is at least R. Else row_src [R]
+ *   int32 and src(r) = row_src[r] / row_div: with perm and k of moe_permute, token perm[r] / k, so
+ *   the routed rows need not be written out. (moe_grouped_gemm_wgrad: the index is of `rows`; dy
+ *   is in routed order.)
+ * Rows outside every expert's range (behind offsets[E], dropped assignments) are neither read nor
+ * written; an expert without rows has a zero weight gradient.
+ * MOE_EINVAL: a null or misaligned pointer, a pitch below the row's width, an unknown or
+ * inconsistent type, row_div < 1.
+ * ------------------------------------------------------------------------------------------- */
+moe_status moe_grouped_gemm(const moe_gemm_shape* s, moe_elt dt, const void* rows, int64_t ld_rows,
+                            const int32_t* row_src, int32_t row_div, int32_t src_rows,
+                            const void* w, const int32_t* offsets, void* out, int64_t ld_out,
+                            moe_elt out_dt, void* stream);
+moe_status moe_grouped_gemm_dgrad(const moe_gemm_shape* s, moe_elt dt, const void* dy,
+                                  int64_t ld_dy, const int32_t* row_src, int32_t row_div,
+                                  int32_t src_rows, const void* w, const int32_t* offsets,
+                                  void* dx, int64_t ld_dx, moe_elt out_dt, void* stream);
+moe_status moe_grouped_gemm_wgrad(const moe_gemm_shape* s, moe_elt dt, const void* rows,
+                                  int64_t ld_rows, const int32_t* row_src, int32_t row_div,
+                                  int32_t src_rows, const void* dy, int64_t ld_dy,
+                                  const int32_t* offsets, void* dw, moe_elt dw_dt, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Int8 products with a scale per token and per weight column.
+ *
+ * moe_quantize_int8: of each row v of x, scale = amax |v| / 127 and code = round(127 v / amax), to
+ *   nearest, ties to even; a row of zeros has scale 0. x [R][K] (pitch ld_x) bf16 or fp16; with
+ *   swiglu = 1 x is [R][2K] = [G | U] and v = silu(G) * U in float32. codes [R][moe_int8_pitch(K)],
+ *   zero behind K; scales [R] float. A row that holds an infinity or a NaN has a scale that is not
+ *   finite, and so are its products. MOE_EUNSUPPORTED: K > 16384.
+ * moe_int8_pitch(K): bytes between code rows, K rounded up to 128 (0 for K < 1).
+ * moe_int8_pack_weights: w_codes [E][N][K] int8 (row n = output column n, as a quantised checkpoint
+ *   holds them; scales [E][N] stay the caller's) into the layout the products read,
+ *   moe_int8_weight_bytes() bytes: blocks of 16 columns x 128 k, zero-padded.
+ * moe_int8_prepare_weights: the same from w [E][K][N] bf16 (y = x W), quantised per column as the
+ *   rows above; w_scales [E][N] float is written.
+ * moe_gemm_int8: out[r][n] = (sum_k codes[r][k] q[n][k]) scales[r] w_scales[n] + bias[n], E = 1,
+ *   one row of codes per output row. moe_grouped_gemm_int8: the same per expert, rows gathered as
+ *   in moe_grouped_gemm (codes and scales [src_rows]). bias [E][N] float or NULL. The integer sum
+ *   is exact in 32 bits. out [R][N] (pitch ld_out), bf16, fp16 or float32.
+ *   MOE_EUNSUPPORTED: K > 131071 (the sum could leave 32 bits). MOE_EINVAL: as above, or E != 1 in
+ *   moe_gemm_int8.
+ * ------------------------------------------------------------------------------------------- */
+size_t moe_int8_pitch(int32_t K);
+moe_status moe_quantize_int8(int32_t R, int32_t K, moe_elt dt, const void* x, int64_t ld_x,
+                             int swiglu, int8_t* codes, float* scales, void* stream);
+size_t moe_int8_weight_bytes(const moe_gemm_shape* s);
+moe_status moe_int8_pack_weights(const moe_gemm_shape* s, const int8_t* w_codes, void* packed,
+                                 void* stream);
+moe_status moe_int8_prepare_weights(const moe_gemm_shape* s, const uint16_t* w, void* packed,
+                                    float* w_scales, void* stream);
+moe_status moe_gemm_int8(const moe_gemm_shape* s, const int8_t* codes, const float* scales,
+                         const void* packed, const float* w_scales, const float* bias, void* out,
+                         int64_t ld_out, moe_elt out_dt, void* stream);
+moe_status moe_grouped_gemm_int8(const moe_gemm_shape* s, const int8_t* codes, const float* scales,
+                                 const int32_t* row_src, int32_t row_div, int32_t src_rows,
+                                 const int32_t* offsets, const void* packed, const float* w_scales,
+                                 const float* bias, void* out, int64_t ld_out, moe_elt out_dt,
+                                 void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Norms before and after a block, with the block's gate and residual scale. T tokens of width h
+ * (any 1 <= h <= 16384, else MOE_EUNSUPPORTED), dense [T][h] bf16 or fp16 (dt). w, gate, w_next:
+ * [h] of type dt or NULL (ones). eps in (0, 1). Sums are float32 in a fixed order.
+ *
+ * moe_pre_norm: z = x rstd w with rstd = (mean x^2 + eps)^(-1/2). z [T][h] and/or its int8 form
+ *   codes [T][moe_int8_pitch(h)] + scales [T] (of the unrounded z, as moe_quantize_int8); at least
+ *   one of them. rstd [T] float or NULL is what the backward pass reads.
+ * moe_post_norm: u = res_scale res + (y rstd w) gate token_gate, rstd = (mean y^2 + eps)^(-1/2),
+ *   rounded once; gate [h] per channel, token_gate [T] float per token, either or both NULL. With z
+ *   or codes, also the next block's pre-norm of the stored u with w_next: the same values as
+ *   moe_pre_norm(u).
+ * moe_pre_norm_backward: dx = d_res + the gradient of x through z (d_res, the gradient that
+ *   arrives at x past the norm, or NULL); dw [h] float or NULL.
+ * moe_post_norm_backward: du the gradient of u (or NULL) and dz that of z (or NULL, then u,
+ *   rstd_next, w_next and dw_next are NULL; u is the stored output); at least one of them. Outputs
+ *   dres and dy [T][h] dt, and dw, dgate, dw_next [h] float, dtoken_gate [T] float, each or NULL.
+ *   The gradients over tokens are summed in a fixed order.
+ * ws: moe_norm_backward_workspace_bytes() bytes.
+ * ------------------------------------------------------------------------------------------- */
+moe_status moe_pre_norm(int32_t T, int32_t h, moe_elt dt, const void* x, const void* w, float eps,
+                        void* z, int8_t* codes, float* scales, float* rstd, void* stream);
+moe_status moe_post_norm(int32_t T, int32_t h, moe_elt dt, const void* res, const void* y,
+                         const void* w, const void* gate, const float* token_gate, float res_scale,
+                         float eps, void* u, float* rstd, const void* w_next, void* z,
+                         int8_t* codes, float* scales, float* rstd_next, void* stream);
+size_t moe_norm_backward_workspace_bytes(int32_t T, int32_t h);
+moe_status moe_pre_norm_backward(int32_t T, int32_t h, moe_elt dt, const void* dz, const void* x,
+                                 const float* rstd, const void* w, const void* d_res, void* dx,
+                                 float* dw, void* ws, void* stream);
+moe_status moe_post_norm_backward(int32_t T, int32_t h, moe_elt dt, const void* du, const void* y,
+                                  const float* rstd, const void* w, const void* gate,
+                                  const float* token_gate, float res_scale, const void* dz,
+                                  const void* u, const float* rstd_next, const void* w_next,
+                                  void* dres, void* dy, float* dw, float* dgate,
+                                  float* dtoken_gate, float* dw_next, void* ws, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

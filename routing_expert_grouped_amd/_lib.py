@@ -14,6 +14,7 @@ LIB_PATH = os.path.join(PKG, "libmoe_mi355x.so")
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EHIP, MOE_ENOSCRATCH, MOE_ETIMEOUT = 0, 1, 2, 3, 4, 5
 MOE_PERMUTE_STATIC_SCRATCH_BYTES = 8 << 20
 MOE_BF16, MOE_MXFP8 = 0, 1
+MOE_ELT_BF16, MOE_ELT_FP16, MOE_ELT_F32 = 0, 1, 2
 
 # every function the header declares, for the symbol check
 EXPORTS = [
@@ -29,6 +30,11 @@ EXPORTS = [
     "moe_saved_bytes", "moe_prepared_bwd_weight_bytes", "moe_prepare_bwd_weights",
     "moe_backward_workspace_bytes", "moe_backward", "moe_backward_layer",
     "moe_backward_profiled",
+    "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad",
+    "moe_int8_pitch", "moe_quantize_int8", "moe_int8_weight_bytes", "moe_int8_pack_weights",
+    "moe_int8_prepare_weights", "moe_gemm_int8", "moe_grouped_gemm_int8",
+    "moe_pre_norm", "moe_post_norm", "moe_norm_backward_workspace_bytes",
+    "moe_pre_norm_backward", "moe_post_norm_backward",
 ]
 
 MOE_PROFILE_EVENTS = 10
@@ -43,6 +49,11 @@ class MoeShape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("h", ctypes.c_int32), ("m", ctypes.c_int32),
                 ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("E_loc", ctypes.c_int32),
                 ("m_shared", ctypes.c_int32)]
+
+
+class MoeGemmShape(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("E", ctypes.c_int32)]
 
 
 class MoeForwardViews(ctypes.Structure):
@@ -71,6 +82,7 @@ def load() -> ctypes.CDLL:
             "(the MoE path has no CPU fallback)")
     lib = ctypes.CDLL(LIB_PATH)
     P, S, I, Z = ctypes.c_void_p, ctypes.POINTER(MoeShape), ctypes.c_int, ctypes.c_size_t
+    Q, N, L, F = ctypes.POINTER(MoeGemmShape), ctypes.c_int32, ctypes.c_int64, ctypes.c_float
     sig = {
         "moe_status_string": (ctypes.c_char_p, [I]),
         "moe_abi_version": (I, []),
@@ -101,6 +113,22 @@ def load() -> ctypes.CDLL:
         "moe_backward": (I, [S, I, P, P, P, P, P, P, P, P, I, P, P]),
         "moe_backward_layer": (I, [S, I, P, P, P, P, P, P, P, P, P, I, P, P, P, P, P]),
         "moe_backward_profiled": (I, [S, I, P, P, P, P, P, P, P, P, I, P, P, P]),
+        "moe_grouped_gemm": (I, [Q, I, P, L, P, N, N, P, P, P, L, I, P]),
+        "moe_grouped_gemm_dgrad": (I, [Q, I, P, L, P, N, N, P, P, P, L, I, P]),
+        "moe_grouped_gemm_wgrad": (I, [Q, I, P, L, P, N, N, P, L, P, P, I, P]),
+        "moe_int8_pitch": (Z, [N]),
+        "moe_quantize_int8": (I, [N, N, I, P, L, I, P, P, P]),
+        "moe_int8_weight_bytes": (Z, [Q]),
+        "moe_int8_pack_weights": (I, [Q, P, P, P]),
+        "moe_int8_prepare_weights": (I, [Q, P, P, P, P]),
+        "moe_gemm_int8": (I, [Q, P, P, P, P, P, P, L, I, P]),
+        "moe_grouped_gemm_int8": (I, [Q, P, P, P, N, N, P, P, P, P, P, L, I, P]),
+        "moe_pre_norm": (I, [N, N, I, P, P, F, P, P, P, P, P]),
+        "moe_post_norm": (I, [N, N, I, P, P, P, P, P, F, F, P, P, P, P, P, P, P, P]),
+        "moe_norm_backward_workspace_bytes": (Z, [N, N]),
+        "moe_pre_norm_backward": (I, [N, N, I, P, P, P, P, P, P, P, P, P]),
+        "moe_post_norm_backward": (I, [N, N, I, P, P, P, P, P, P, F, P, P, P, P, P, P, P, P, P, P,
+                                       P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
