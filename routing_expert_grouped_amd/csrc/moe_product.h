@@ -2,8 +2,8 @@
 // share (operand kinds, argument block, expert lookup, fragment reads, output stores).
 //
 // Every product here is out[m][n] = sum_k M[m][k] N[n][k] per expert, with the n operand as the
-// MFMA's A matrix and the m operand as its B matrix: a lane of a 32 x 32 MFMA then holds one output
-// row m and four runs of four consecutive columns n.
+// MFMA's A matrix and the m operand as its B matrix: a lane of a 16 x 16 MFMA then holds one output
+// row m and four consecutive columns n.
 //   forward   out[r][n]  : m = routed rows (K-contiguous), n = columns of W [K][N] (K-strided)
 //   input grad dX[r][k'] : m = rows of dY, n = rows of W [K][N], the sum along N: both contiguous
 //   weight grad dW[k'][n]: m = columns of X, n = columns of dY, the sum over the expert's rows:
@@ -61,35 +61,38 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
-typedef int i32x16_t __attribute__((ext_vector_type(16)));
+typedef int i32x4v_t __attribute__((ext_vector_type(4)));
+typedef float f32x4v_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef u32x4_t u32x4_any_t __attribute__((aligned(1)));  // a 16-byte load from any address
 
 template <int EL>
 struct ProductTypes {
   static constexpr int kBytes = 2;
-  using Acc = f32x16_t;
+  using Acc = f32x4v_t;
 };
 template <>
 struct ProductTypes<kPeI8> {
   static constexpr int kBytes = 1;
-  using Acc = i32x16_t;
+  using Acc = i32x4v_t;
 };
 
-// one 32 x 32 MFMA step over 32 bytes of k per row (16 of each lane half): 16 elements of 16 bits,
-// or 32 int8 elements summed exactly in 32-bit integers
+// One 16 x 16 MFMA step over 64 bytes of k per row (16 of each 16 lanes): 32 elements of 16 bits, or
+// 64 int8 elements summed exactly in 32-bit integers. The 16 x 16 form sums twice the k of the
+// 32 x 32 form into each accumulator it touches and draws less power for it, which is what bounds
+// a large product here (8192^3 bf16, both operands contiguous: see moe_product_big.h).
 template <int EL>
 __device__ __forceinline__ typename ProductTypes<EL>::Acc product_mfma(
     u32x4_t a, u32x4_t b, typename ProductTypes<EL>::Acc c) {
 #if defined(__HIP_DEVICE_COMPILE__)
   if constexpr (EL == kPeBf16) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                    __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
   } else if constexpr (EL == kPeFp16) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a),
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a),
                                                   __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
   } else {
-    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, a),
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a),
                                                  __builtin_bit_cast(i32x4_t, b), c, 0, 0, 0);
   }
 #else
@@ -100,19 +103,21 @@ __device__ __forceinline__ typename ProductTypes<EL>::Acc product_mfma(
 
 // ------------------------------------------------------------------------------------------------
 // LDS image of one operand stage: 128 bytes of k (64 elements of 16 bits, 128 of 8) for ROWS rows.
-//   contiguous kinds: row r is 128 bytes, 16-byte chunk c at slot c ^ f(r): the 32 rows a fragment
-//     read touches at one chunk then spread over all banks;
+//   contiguous kinds: row r is 128 bytes, 16-byte chunk c at slot c ^ f(r) with f(r) = r / 2 mod 8:
+//     the 16 rows that a phase of a fragment read touches at one chunk lie on 16 different
+//     16-byte groups of the 64 banks, and f(r + 16) = f(r), so a wave's fragments are one lane
+//     address and constant offsets;
 //   strided kind: k row kk is ROWS * 2 bytes, in slots of 32 bytes (16 columns), slot s at
-//     s ^ g(kk). A transposing read takes, per 16 lanes, four k rows of one slot; g spreads the
-//     eight slots that 32 lanes read over all 64 banks.
+//     s ^ g(kk). A transposing read takes, per 16 lanes, four k rows of one slot, 32 lanes k rows
+//     kk .. kk + 3 and kk + 8 .. kk + 11; g spreads those eight slots over all 64 banks.
 // ------------------------------------------------------------------------------------------------
-__device__ __forceinline__ int kc_swizzle(int row) { return (row ^ (row >> 3)) & 7; }
+__device__ __forceinline__ int kc_swizzle(int row) { return (row >> 1) & 7; }
 
 template <int ROWS>
 __device__ __forceinline__ int ks_swizzle(int kk) {
-  if constexpr (ROWS >= 128) return 2 * (kk & 3);
-  else if constexpr (ROWS == 64) return 2 * ((kk >> 1) & 1);
-  else return 0;
+  if constexpr (ROWS >= 128) return 2 * (kk & 3) + ((kk >> 3) & 1);
+  else if constexpr (ROWS == 64) return (kk & 2) + ((kk >> 3) & 1);
+  else return (kk >> 3) & 1;
 }
 
 // byte of 16-byte chunk `id` of a stage image (id = row * 8 + c, or kk * (ROWS / 8) + c)
@@ -128,31 +133,38 @@ __device__ __forceinline__ int stage_byte(int id) {
   }
 }
 
-// the 16 bytes of MFMA step t (0..3) of a stage for this lane: row r0 + lane % 32, k bytes
-// 32 t + 16 (lane / 32) .. + 16. The transposing read gives lane i of 16 column i of the block
-// whose four k rows the 16 lanes address (lane j: row j / 4, columns 4 (j % 4) ..).
+// Fragment i of a wave at MFMA step t (0 or 1) of a stage: row r0 + 16 i + lane % 16, k bytes
+// 64 t + 16 (lane / 16) .. + 16, r0 a multiple of the wave's rows. fragment_base is the lane's part
+// of the address. The transposing read gives lane j of 16 column j of the block whose four k rows
+// the 16 lanes address (lane j: row j / 4, columns 4 (j % 4) ..).
 template <int KIND, int ROWS>
-__device__ __forceinline__ u32x4_t read_fragment(const uint8_t* stage, int r0, int t, int lane) {
-#if defined(__HIP_DEVICE_COMPILE__)
+__device__ __forceinline__ int fragment_base(int r0, int lane) {
   if constexpr (KIND == kOpKs) {
     const int i = lane & 15;
-    const int kk = 16 * t + 8 * (lane >> 5) + (i >> 2);
-    const int slot = (r0 >> 4) + ((lane >> 4) & 1);
-    const uint8_t* p0 = stage + kk * (ROWS * 2) + ((slot ^ ks_swizzle<ROWS>(kk)) << 5) +
-                        ((i & 3) << 3);
-    const uint8_t* p1 = stage + (kk + 4) * (ROWS * 2) +
-                        ((slot ^ ks_swizzle<ROWS>(kk + 4)) << 5) + ((i & 3) << 3);
+    const int kk = 8 * (lane >> 4) + (i >> 2);
+    return kk * (ROWS * 2) + (((r0 >> 4) ^ ks_swizzle<ROWS>(kk)) << 5) + ((i & 3) << 3);
+  } else {
+    const int row = r0 + (lane & 15);
+    return row * 128 + (((lane >> 4) ^ kc_swizzle(row)) << 4);
+  }
+}
+
+template <int KIND, int ROWS>
+__device__ __forceinline__ u32x4_t read_fragment(const uint8_t* stage, int base, int i, int t) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if constexpr (KIND == kOpKs) {
+    // (slot i only touches address bits that the slot of r0 leaves zero)
+    const uint8_t* p0 = stage + (base ^ (i << 5)) + t * (32 * ROWS * 2);
     const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)p0);
-    const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)p1);
+    const s16x4_t b =
+        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p0 + 4 * (ROWS * 2)));
     const s16x8_t v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     return __builtin_bit_cast(u32x4_t, v);
   } else {
-    const int row = r0 + (lane & 31);
-    const int c = 2 * t + (lane >> 5);
-    return *reinterpret_cast<const u32x4_t*>(stage + row * 128 + ((c ^ kc_swizzle(row)) << 4));
+    return *reinterpret_cast<const u32x4_t*>(stage + (base ^ (t << 6)) + i * 2048);
   }
 #else
-  (void)stage, (void)r0, (void)t, (void)lane;
+  (void)stage, (void)base, (void)i, (void)t;
   return u32x4_t{};
 #endif
 }
@@ -186,14 +198,16 @@ __device__ __forceinline__ void expert_rows(const ProductArgs& p, int e, int& lo
   hi = min(max(p.offsets[e + 1], lo), p.R);
 }
 
-// The M tile table in LDS: first tile of each expert, by one scan per workgroup (256 threads, four
-// experts each). Cheaper than a launch of its own for a small call and invisible in a large one.
+// The M tile table: first tile of each expert, by one scan per workgroup (the first 256 threads,
+// four experts each; scratch: one int per wave). Cheaper than a launch of its own for a small call
+// and invisible in a large one.
 struct TileIndex {
   int first[4];  // this thread's experts: first tile of expert 4 tid + q
   int next;      // first tile after them
   int total;     // M tiles of all experts
 };
 
+template <int WAVES>
 __device__ __forceinline__ TileIndex tile_index(const ProductArgs& p, int bm, int* scratch) {
   TileIndex x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -218,11 +232,12 @@ __device__ __forceinline__ TileIndex tile_index(const ProductArgs& p, int bm, in
   if (lane == 63) scratch[wave] = inc;
   __syncthreads();
   int base = 0;
+  x.total = 0;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < WAVES; ++w) {
     if (w < wave) base += scratch[w];
+    x.total += scratch[w];
   }
-  x.total = scratch[0] + scratch[1] + scratch[2] + scratch[3];
   __syncthreads();
   int f = base + inc - sum;
 #pragma unroll
@@ -275,7 +290,6 @@ __device__ __forceinline__ int source_row(const ProductArgs& p, int r) {
 // ------------------------------------------------------------------------------------------------
 typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
-typedef float f32x4v_t __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ uint2 round_bf16x4(f32x4v_t v) {
   return __builtin_bit_cast(uint2, __builtin_convertvector(v, bf16x4_t));

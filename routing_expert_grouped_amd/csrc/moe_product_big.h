@@ -1,0 +1,416 @@
+// The large tile of the ragged grouped products: BN output columns x BM output rows per workgroup,
+// operands brought from memory straight into two rings of LDS stages.
+//
+// A stage is 128 bytes of the sum index of one operand (the image of moe_product.h). Whole stages
+// are copied by the DMA form of the global load (16 bytes per lane, 1 KB of consecutive LDS per
+// wave and instruction; the image's swizzle is applied by choosing which chunk a lane fetches),
+// NSN - 1 (n operand) and NSM - 1 (m operand) stages ahead of the MFMAs. In a last, partial stage (a
+// sum length that is no multiple of a stage, and every expert's rows in a weight gradient) the
+// lanes whose chunk lies behind the end fetch 16 zero bytes instead. Rows and columns behind the
+// tile's edge are fetched from its last row or chunk and never stored.
+//
+// Order. Each of a stage's two MFMA steps multiplies fragments that were read during the step
+// before it; between its MFMAs go the LDS reads of the next step and half of the loads of the
+// stages ahead, one by one: a wave issues in order, and a run of loads stalls it (and its MFMAs)
+// at the rate the memory path takes them, 16 clocks per KB.
+//
+// Waits. The compiler does not order the direct LDS writes against LDS reads. Loads return in issue
+// order, so at point j (before the last MFMA step of stage j - 1) a count says that this wave's
+// parts of stage j are in LDS; the barrier after it says so for all waves, and that every wave has
+// read its fragments of stage j - 1, whose ring slots the loads issued next overwrite.
+#pragma once
+
+#include "moe_gemm_big.h"
+#include "moe_product.h"
+
+namespace moe {
+namespace {
+
+// 16-byte direct load of one lane to LDS from a uniform base and a 32-bit lane offset; the wave's
+// lanes fill 1 KB from LDS byte address `l`. Written as assembly because the compiler would put a
+// wait for every direct load in flight before each transposing LDS read (it cannot tell their
+// places apart). Nothing but LDS is written, and the compiler's own counted waits only get
+// stricter by loads it does not count. (One idle state between the write of M0 and its use. M0 is
+// no allocatable register: the compiler sets it where it needs it itself.)
+__device__ __forceinline__ void dma16_at(const uint8_t* base, uint32_t off, uint32_t l) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(l), "v"(off), "s"(base)
+               : "memory");
+#else
+  (void)base, (void)off, (void)l;
+#endif
+}
+
+// the same from a 64-bit lane address
+__device__ __forceinline__ void dma16_from(const uint8_t* g, uint32_t l) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(l), "v"(g)
+               : "memory");
+#else
+  (void)g, (void)l;
+#endif
+}
+
+// what lanes behind the end of a sum fetch
+__device__ __attribute__((aligned(16))) const uint8_t kZeroChunk[16] = {};
+
+// byte address of a place in LDS
+__device__ __forceinline__ uint32_t lds_address(const uint8_t* l) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef __attribute__((address_space(3))) const uint8_t lds_u8_t;
+  return (uint32_t)(uintptr_t)(lds_u8_t*)l;
+#else
+  (void)l;
+  return 0;
+#endif
+}
+
+// product_mfma with the accumulators held in the accumulator registers: 256 of them per lane are all
+// there are, and left to itself the compiler moves some through vector registers around every
+// MFMA. What the compiler does not see of such an MFMA: its result may be read by another
+// instruction only after the unit's latency (acc_settle below), and a register it reads as
+// accumulator only that long after a vector write.
+template <int EL>
+__device__ __forceinline__ void product_mfma_acc(u32x4_t a, u32x4_t b,
+                                                 typename ProductTypes<EL>::Acc& c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if constexpr (EL == kPeBf16)
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+  else if constexpr (EL == kPeFp16)
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+  else
+    asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+#else
+  (void)a, (void)b, (void)c;
+#endif
+}
+
+// more than the longest MFMA latency (and than the wait before an MFMA reads a written accumulator)
+__device__ __forceinline__ void acc_settle() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#endif
+}
+
+template <class Acc>
+__device__ __forceinline__ void acc_pin(Acc& c) {  // c is in its accumulator registers here
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+a"(c));
+#endif
+}
+
+template <int EL, int NK, int MK, int BN, int BM, int WN, int WM, int NSN, int NSM>
+struct ProductBig {
+  static constexpr int kWaves = WN * WM;
+  static constexpr int kThreads = 64 * kWaves;
+  static constexpr int TN = BN / WN, TM = BM / WM;  // a wave's tile
+  static constexpr int NI = TN / 16, NJ = TM / 16;
+  static constexpr int NQ = BN * 8 / kThreads;      // 16-byte chunks per thread and stage
+  static constexpr int MQ = BM * 8 / kThreads;
+  static constexpr int EB = ProductTypes<EL>::kBytes;
+  static constexpr int BK = 128 / EB;
+  static constexpr int kNStage = BN * 128, kMStage = BM * 128;
+  static constexpr bool kWgrad = MK == kOpKs;
+  // epilogue: a wave's 32 rows x TN columns of float32, rows padded by 16 bytes
+  static constexpr int kEpiPitch = TN * 4 + 16;
+  static constexpr int kEpi = kWaves * 32 * kEpiPitch;
+  static constexpr int kRings = NSN * kNStage + NSM * kMStage;
+  static constexpr int kLds = kRings > kEpi ? kRings : kEpi;
+  // loads that may be in flight at a point: those issued after the stage it waits for. A point
+  // issues its m stage, then its n stage.
+  static constexpr int kFlying = (NSM == 3 ? MQ : 0) + (NSN == 3 ? NQ : 0);
+  static_assert(kLds <= 160 * 1024, "LDS budget");
+  static_assert(NQ * kThreads == BN * 8 && MQ * kThreads == BM * 8, "whole chunks");
+  static_assert((NSN == 2 || NSN == 3) && (NSM == 2 || (NSM == 3 && NSN == 3)), "ring depths");
+  static_assert(kFlying < 64, "vmcnt range");
+  using Acc = typename ProductTypes<EL>::Acc;
+
+  // chunk `id` of a stage image in LDS order: the k row (strided) or row (contiguous) it belongs
+  // to, and the logical chunk within that row whose place this is
+  template <int KIND, int ROWS>
+  static __device__ __forceinline__ void chunk_of(int id, int& row, int& c) {
+    if constexpr (KIND == kOpKs) {
+      constexpr int CPR = ROWS / 8;
+      row = id / CPR;
+      const int pc = id % CPR;
+      c = ((((pc >> 1) ^ ks_swizzle<ROWS>(row)) << 1) | (pc & 1));
+    } else {
+      row = id >> 3;
+      c = (id & 7) ^ kc_swizzle(row);
+    }
+  }
+
+  struct Frags {
+    u32x4_t a[NI], b[NJ];
+  };
+
+  static __device__ __forceinline__ void run(const ProductArgs& p, int e, int row0, int row_end,
+                                             int n0, uint8_t* lds) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave / WM, wm = wave % WM;
+    int k_lo = 0, k_hi = p.K;
+    if constexpr (kWgrad) expert_rows(p, e, k_lo, k_hi);
+    const int klen = __builtin_amdgcn_readfirstlane(k_hi - k_lo);
+    const int whole = klen / BK;
+    const bool part = klen % BK != 0;
+    const int stages = whole + (part ? 1 : 0);
+
+    // uniform operand bases of the tile, per-lane byte offsets from them, bytes per stage
+    const uint8_t* nb = p.n_base + (size_t)e * p.n_estride;
+    size_t nstep;
+    uint32_t noff[NQ];
+    if constexpr (NK == kOpKs) {
+      nb += (size_t)k_lo * p.n_pitch + (size_t)n0 * EB;
+      nstep = (size_t)BK * p.n_pitch;
+    } else if constexpr (NK == kOpPanel) {
+      nb += (size_t)(n0 >> 4) * p.n_pitch;
+      nstep = 2048;
+    } else {
+      nb += (size_t)n0 * p.n_pitch;
+      nstep = 128;
+    }
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      int row, c;
+      chunk_of<NK, BN>(q * kThreads + tid, row, c);
+      if constexpr (NK == kOpKs) {
+        noff[q] = (uint32_t)(row * (int)p.n_pitch + min(8 * c, p.N - n0 - 8) * EB);
+      } else {
+        const int r = min(row, p.N - 1 - n0);
+        if constexpr (NK == kOpPanel)
+          noff[q] = (uint32_t)((r >> 4) * (int)p.n_pitch + (r & 15) * 128 + 16 * c);
+        else
+          noff[q] = (uint32_t)(r * (int)p.n_pitch + 16 * c);
+      }
+    }
+    const uint8_t* mb = p.m_base;
+    size_t mstep = 128;
+    uint32_t moff[MQ];
+    if constexpr (kWgrad) {
+      mb += (size_t)k_lo * p.m_pitch + (size_t)row0 * EB;
+      mstep = (size_t)BK * p.m_pitch;
+    } else if (!p.row_src) {
+      mb += (size_t)row0 * p.m_pitch;
+    }
+#pragma unroll
+    for (int q = 0; q < MQ; ++q) {
+      int row, c;
+      chunk_of<MK, BM>(q * kThreads + tid, row, c);
+      if constexpr (kWgrad) {
+        moff[q] = (uint32_t)(row * (int)p.m_pitch + min(8 * c, p.M - row0 - 8) * EB);
+      } else {
+        const int r = min(row0 + row, row_end - 1);
+        moff[q] = (uint32_t)((p.row_src ? source_row(p, r) : r - row0) * (uint32_t)p.m_pitch +
+                             16 * c);
+      }
+    }
+    nb = uniform_ptr(nb);
+    mb = uniform_ptr(mb);
+
+    const uint32_t ring = __builtin_amdgcn_readfirstlane(lds_address(lds));
+    auto nslot = [&](int j) { return (j % NSN) * kNStage; };
+    auto mslot = [&](int j) { return NSN * kNStage + (j % NSM) * kMStage; };
+    auto load_n = [&](int j, int q) {
+      dma16_at(nb + (size_t)j * nstep, noff[q], ring + nslot(j) + (q * kWaves + wave) * 1024);
+    };
+    auto load_m = [&](int j, int q) {
+      dma16_at(mb + (size_t)j * mstep, moff[q], ring + mslot(j) + (q * kWaves + wave) * 1024);
+    };
+    // the same for a stage that may be the partial one (chunks are whole or absent)
+    const int left = klen - whole * BK;
+    auto load_n_any = [&](int j, int q) {
+      int row, c;
+      chunk_of<NK, BN>(q * kThreads + tid, row, c);
+      const bool there = j < whole || NK == kOpPanel ||
+                         (NK == kOpKs ? row < left : c * (16 / EB) < left);
+      dma16_from(there ? nb + (size_t)j * nstep + noff[q] : kZeroChunk,
+                 ring + nslot(j) + (q * kWaves + wave) * 1024);
+    };
+    auto load_m_any = [&](int j, int q) {
+      int row, c;
+      chunk_of<MK, BM>(q * kThreads + tid, row, c);
+      const bool there = j < whole || EL == kPeI8 ||
+                         (MK == kOpKs ? row < left : c * (16 / EB) < left);
+      dma16_from(there ? mb + (size_t)j * mstep + moff[q] : kZeroChunk,
+                 ring + mslot(j) + (q * kWaves + wave) * 1024);
+    };
+
+    Acc acc[NI][NJ];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = 0;
+#pragma unroll
+    for (int i = 0; i < NI * NJ; ++i) acc_pin(acc[i / NJ][i % NJ]);
+    acc_settle();
+
+    const int nfrag = fragment_base<NK, BN>(wn * TN, lane);
+    const int mfrag = fragment_base<MK, BM>(wm * TM, lane);
+    auto read_one = [&](Frags& f, const uint8_t* ns, const uint8_t* ms, int t, int i) {
+      if (i < NI) f.a[i] = read_fragment<NK, BN>(ns, nfrag, i, t);
+      else f.b[i - NI] = read_fragment<MK, BM>(ms, mfrag, i - NI, t);
+    };
+
+    // Point j: the wait and barrier that make stage j readable, then its loads, m stage j + NSM - 1
+    // and n stage j + NSN - 1: part 0 of them behind the barrier, in the last step of stage j - 1,
+    // part 1 in the first step of stage j.
+    constexpr int U = MQ + NQ;
+    auto load_unit = [&](int j, int u) {  // unit u of point j's loads, whole stages
+      if (u < MQ) load_m(j + NSM - 1, u);
+      else load_n(j + NSN - 1, u - MQ);
+    };
+    auto load_part = [&](int j, int part) {  // part 0 or 1 of point j's loads, where they exist
+#pragma unroll
+      for (int u = part * U / 2; u < (part + 1) * U / 2; ++u) {
+        if (u < MQ) {
+          if (j + NSM - 1 < stages) load_m_any(j + NSM - 1, u);
+        } else {
+          if (j + NSN - 1 < stages) load_n_any(j + NSN - 1, u - MQ);
+        }
+      }
+    };
+    auto point = [&](int j) {
+      if (j + 1 < stages) wait_vmcnt_fenced<kFlying>();
+      else wait_vmcnt_fenced<0>();
+      lds_barrier();
+    };
+
+    // step t of stage j on fragments `cur`: its MFMAs with, between them, the reads of the next
+    // step into `nxt` and a part of the loads of the current point
+    constexpr int NM = NI * NJ, NR = NI + NJ;
+    auto step = [&](int j, auto t_tag, auto steady, Frags& cur, Frags& nxt) {
+      constexpr int t = decltype(t_tag)::value;
+      constexpr bool S = decltype(steady)::value;
+      constexpr bool LAST = t == 1;
+      constexpr int PART = LAST ? 0 : 1;                // part of the point's loads sent here
+      constexpr int D0 = PART * U / 2, ND = S ? (PART + 1) * U / 2 - D0 : 0;
+      constexpr int OPS = NR + ND;
+      constexpr int SLOTS = NM - NM / 8;                // (the last MFMAs cover the last reads)
+      const bool more = !LAST || j + 1 < stages;        // (STEADY: always)
+      const uint8_t* ns = lds + nslot(LAST ? j + 1 : j);
+      const uint8_t* ms = lds + mslot(LAST ? j + 1 : j);
+      const int dj = LAST ? j + 1 : j;                  // whose point's loads go out here
+      if (!S && !LAST) load_part(j, 1);
+      if (!S && LAST && more) {
+        point(j + 1);
+        load_part(j + 1, 0);
+      }
+#pragma unroll
+      for (int m = 0; m < NM; ++m) {
+        product_mfma_acc<EL>(cur.a[m / NJ], cur.b[m % NJ], acc[m / NJ][m % NJ]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (S && LAST && m == 0) {
+          wait_vmcnt_fenced<kFlying>();
+          lds_barrier();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (!S && !more) continue;
+#pragma unroll
+        for (int op = m * OPS / SLOTS; op < (m + 1) * OPS / SLOTS; ++op) {
+          // reads and loads in turn, the rest of the longer list last
+          if (op < OPS) {
+            constexpr int PAIRS = 2 * (ND < NR ? ND : NR);
+            const bool load = op < PAIRS ? op % 2 == 1 : ND > NR;
+            const int at = op < PAIRS ? op / 2 : op - PAIRS / 2;
+            if (load) load_unit(dj, D0 + at);
+            else read_one(nxt, ns, ms, LAST ? 0 : t + 1, at);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    auto stage = [&](int j, auto steady, Frags& f0, Frags& f1) {
+      step(j, std::integral_constant<int, 0>{}, steady, f0, f1);
+      step(j, std::integral_constant<int, 1>{}, steady, f1, f0);
+    };
+
+    if (stages > 0) {
+#pragma unroll
+      for (int j = 1 - NSN; j < 0; ++j) {  // the points before 0
+        if (j + NSM - 1 >= 0 && j + NSM - 1 < stages) {
+#pragma unroll
+          for (int q = 0; q < MQ; ++q) load_m_any(j + NSM - 1, q);
+        }
+        if (j + NSN - 1 < stages) {
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) load_n_any(j + NSN - 1, q);
+        }
+      }
+      Frags f0, f1;
+      point(0);
+      load_part(0, 0);
+#pragma unroll
+      for (int i = 0; i < NR; ++i) read_one(f0, lds + nslot(0), lds + mslot(0), 0, i);
+      int j = 0;
+      for (; j + NSN < whole; ++j) stage(j, std::true_type{}, f0, f1);
+      for (; j < stages; ++j) stage(j, std::false_type{}, f0, f1);
+    }
+    lds_barrier();  // every fragment is read: LDS is free for the epilogue
+    acc_settle();
+#pragma unroll
+    for (int i = 0; i < NI * NJ; ++i) acc_pin(acc[i / NJ][i % NJ]);
+
+    // acc[i][j][q]: column n0 + wn TN + 16 i + 4 (lane / 16) + q,
+    //               row row0 + wm TM + 16 j + lane % 16.
+    // Each wave turns its tile through its own part of LDS, 32 rows at a time, so that a store
+    // instruction writes whole 128-byte lines of a few rows.
+    const int row_lim = kWgrad ? p.M : row_end;
+    uint8_t* w = lds + wave * (32 * kEpiPitch);
+#pragma unroll
+    for (int jj = 0; jj < NJ / 2; ++jj) {
+      const int r0 = row0 + wm * TM + 32 * jj;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int lr = 16 * h + (lane & 15);
+        float ms = 1.0f;
+        if constexpr (EL == kPeI8) ms = p.m_scale[source_row(p, min(r0 + lr, row_end - 1))];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          f32x4v_t v;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            v[q] = (float)acc[i][2 * jj + h][q];
+            if constexpr (EL == kPeI8) v[q] *= ms;
+          }
+          *reinterpret_cast<f32x4v_t*>(w + lr * kEpiPitch + (16 * i + 4 * (lane >> 4)) * 4) = v;
+        }
+      }
+      // (the wave's own LDS operations stay in order; the compiler waits for the reads)
+      constexpr int LPR = TN / 4, RPI = 64 / LPR;  // lanes per row, rows per instruction
+      const int c4 = (lane % LPR) * 4, n = n0 + wn * TN + c4;
+      f32x4v_t ns = {1.0f, 1.0f, 1.0f, 1.0f}, bs = {0.0f, 0.0f, 0.0f, 0.0f};
+      if constexpr (EL == kPeI8) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const size_t c = (size_t)e * p.N + min(n + q, p.N - 1);
+          ns[q] = p.n_scale[c];
+          if (p.bias) bs[q] = p.bias[c];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 32 / RPI; ++k) {
+        const int rr = k * RPI + lane / LPR, r = r0 + rr;
+        f32x4v_t v = *reinterpret_cast<const f32x4v_t*>(w + rr * kEpiPitch + c4 * 4);
+        if constexpr (EL == kPeI8) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            v[q] *= ns[q];
+            if (p.bias) v[q] += bs[q];
+          }
+        }
+        if (r < row_lim && n < p.N)
+          store_run(p, ((size_t)r + (kWgrad ? (size_t)e * p.M : 0)) * p.out_ld + n, n, v);
+      }
+    }
+  }
+};
+
+}  // namespace
+}  // namespace moe

@@ -7,7 +7,7 @@
 // double-buffered LDS image. Chunks that pass the end of a row, of the columns or of an expert's
 // rows are zero in LDS, so every size is covered by the same loop and nothing that lies behind an
 // expert's rows (another expert's infinities, unwritten memory) enters a sum.
-#include "moe_product.h"
+#include "moe_product_big.h"
 
 namespace moe {
 namespace {
@@ -15,8 +15,8 @@ namespace {
 template <int EL, int NK, int MK, int BN, int BM, int WN>
 struct ProductTile {
   static constexpr int WM = 4 / WN;            // waves along the rows
-  static constexpr int NI = BN / WN / 32;      // n fragments per wave
-  static constexpr int NJ = BM / WM / 32;      // m fragments per wave
+  static constexpr int NI = BN / WN / 16;      // n fragments per wave
+  static constexpr int NJ = BM / WM / 16;      // m fragments per wave
   static constexpr int NQ = BN * 8 / 256;      // 16-byte chunks per thread and stage, n operand
   static constexpr int MQ = BM * 8 / 256;
   static constexpr int EB = ProductTypes<EL>::kBytes;
@@ -123,8 +123,10 @@ struct ProductTile {
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = 0;
 
+    const int nfrag = fragment_base<NK, BN>(wn * (BN / WN), lane);
+    const int mfrag = fragment_base<MK, BM>(wm * (BM / WM), lane);
     if (stages > 0) {
       fetch(0);
       put(0);
@@ -134,14 +136,14 @@ struct ProductTile {
       if (j + 1 < stages) fetch(j + 1);
       const uint8_t* s = lds + (j & 1) * kStage;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < 2; ++t) {
         u32x4_t a[NI], b[NJ];
 #pragma unroll
         for (int i = 0; i < NI; ++i)
-          a[i] = read_fragment<NK, BN>(s, wn * (BN / WN) + 32 * i, t, lane);
+          a[i] = read_fragment<NK, BN>(s, nfrag, i, t);
 #pragma unroll
         for (int i = 0; i < NJ; ++i)
-          b[i] = read_fragment<MK, BM>(s + BN * 128, wm * (BM / WM) + 32 * i, t, lane);
+          b[i] = read_fragment<MK, BM>(s + BN * 128, mfrag, i, t);
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -150,58 +152,53 @@ struct ProductTile {
       if (j + 1 < stages) put((j + 1) & 1);
     }
 
-    // acc[i][j][q]: column n0 + wn BN/WN + 32 i + 8 (q / 4) + 4 (lane / 32) + q % 4,
-    //               row row0 + wm BM/WM + 32 j + lane % 32
+    // acc[i][j][q]: column n0 + wn BN/WN + 16 i + 4 (lane / 16) + q,
+    //               row row0 + wm BM/WM + 16 j + lane % 16
     const int row_lim = kWgrad ? p.M : row_end;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int r = row0 + wm * (BM / WM) + 32 * j + (lane & 31);
+      const int r = row0 + wm * (BM / WM) + 16 * j + (lane & 15);
       if (r >= row_lim) continue;
       const size_t at = ((size_t)r + (kWgrad ? (size_t)e * p.M : 0)) * p.out_ld;
       float ms = 0.0f;
       if constexpr (EL == kPeI8) ms = p.m_scale[source_row(p, r)];
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
+      for (int i = 0; i < NI; ++i) {
+        const int n = n0 + wn * (BN / WN) + 16 * i + 4 * (lane >> 4);
+        if (n >= p.N) continue;
+        f32x4v_t v;
 #pragma unroll
-        for (int b4 = 0; b4 < 4; ++b4) {
-          const int n = n0 + wn * (BN / WN) + 32 * i + 8 * b4 + 4 * (lane >> 5);
-          if (n >= p.N) continue;
-          f32x4v_t v;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            v[q] = (float)acc[i][j][4 * b4 + q];
-            if constexpr (EL == kPeI8) {
-              const size_t c = (size_t)e * p.N + min(n + q, p.N - 1);
-              v[q] = v[q] * ms * p.n_scale[c];
-              if (p.bias) v[q] += p.bias[c];
-            }
+        for (int q = 0; q < 4; ++q) {
+          v[q] = (float)acc[i][j][q];
+          if constexpr (EL == kPeI8) {
+            const size_t c = (size_t)e * p.N + min(n + q, p.N - 1);
+            v[q] = v[q] * ms * p.n_scale[c];
+            if (p.bias) v[q] += p.bias[c];
           }
-          store_run(p, at + n, n, v);
         }
+        store_run(p, at + n, n, v);
+      }
     }
   }
 };
 
-template <int EL, int NK, int MK, int BN, int BM, int WN>
-__global__ __launch_bounds__(256, 2) void product_tile_kernel(ProductArgs p) {
-  using Tile = ProductTile<EL, NK, MK, BN, BM, WN>;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[Tile::kLds];
-  __shared__ int scratch[4];
+// The tiles of one workgroup: a fixed share of its XCD's part of the tile order (big_tile_coords).
+template <class Tile, int BN, int BM, int WAVES>
+__device__ __forceinline__ void product_tiles(const ProductArgs& p, uint8_t* lds, int* scratch) {
   const int nt_total = (p.N + BN - 1) / BN;
+  const int xcd = blockIdx.x & 7;
+  int ti, nt;
   if constexpr (Tile::kWgrad) {
     const int mt = (p.M + BM - 1) / BM;
-    const int per = mt * nt_total;
-    for (long long t = blockIdx.x; t < (long long)per * p.E; t += gridDim.x) {
-      const int e = (int)(t / per), i = (int)(t % per);
-      Tile::run(p, e, (i / nt_total) * BM, 0, (i % nt_total) * BN, lds);
+    for (int jx = blockIdx.x >> 3;
+         big_tile_coords(mt * p.E, nt_total, p.band_gm, xcd, jx, ti, nt); jx += gridDim.x >> 3) {
+      Tile::run(p, ti / mt, (ti % mt) * BM, 0, nt * BN, lds);
       __syncthreads();
     }
   } else {
-    const TileIndex x = tile_index(p, BM, scratch);
-    const int xcd = blockIdx.x & 7;
-    for (int jx = blockIdx.x >> 3;; jx += gridDim.x >> 3) {
-      int ti, nt;
-      if (!big_tile_coords(x.total, nt_total, p.band_gm, xcd, jx, ti, nt)) break;
+    const TileIndex x = tile_index<WAVES>(p, BM, scratch);
+    for (int jx = blockIdx.x >> 3; big_tile_coords(x.total, nt_total, p.band_gm, xcd, jx, ti, nt);
+         jx += gridDim.x >> 3) {
       int e, row0, row_end;
       tile_lookup(p, x, ti, BM, scratch, e, row0, row_end);
       Tile::run(p, e, row0, row_end, nt * BN, lds);
@@ -210,30 +207,88 @@ __global__ __launch_bounds__(256, 2) void product_tile_kernel(ProductArgs p) {
   }
 }
 
-// workgroups of a persistent launch: at most two per CU of the device, no more than the tiles
-// there can be, and a multiple of 8 (one share per XCD)
-unsigned product_grid(long long tiles) {
-  const long long g = tiles < 512 ? tiles : 512;
+template <int EL, int NK, int MK, int BN, int BM, int WN>
+__global__ __launch_bounds__(256, 2) void product_tile_kernel(ProductArgs p) {
+  using Tile = ProductTile<EL, NK, MK, BN, BM, WN>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Tile::kLds];
+  __shared__ int scratch[4];
+  product_tiles<Tile, BN, BM, 4>(p, lds, scratch);
+}
+
+template <int EL, int NK, int MK, int BN, int BM, int WN, int WM, int NSN, int NSM>
+__global__ __launch_bounds__(64 * WN * WM, WN * WM / 4) void product_big_kernel(ProductArgs p) {
+  using Tile = ProductBig<EL, NK, MK, BN, BM, WN, WM, NSN, NSM>;
+  // one LDS object: beside a second one the compiler waits for every direct load before the next
+  // LDS read. The tile lookup's few words share it with the rings, a barrier apart.
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Tile::kLds];
+  product_tiles<Tile, BN, BM, WN * WM>(p, lds, reinterpret_cast<int*>(lds));
+}
+
+// workgroups of a persistent launch: at most `slots` (those that run at once), no more than the
+// tiles there can be, and a multiple of 8 (one share per XCD)
+unsigned product_grid(long long tiles, long long slots) {
+  const long long g = tiles < slots ? tiles : slots;
   return (unsigned)((g + 7) / 8 * 8);
 }
 
 template <int EL, int NK, int MK, int BN, int BM, int WN>
 hipError_t launch_tile(const ProductArgs& p, long long tiles, hipStream_t st) {
-  hipLaunchKernelGGL((product_tile_kernel<EL, NK, MK, BN, BM, WN>), dim3(product_grid(tiles)),
+  hipLaunchKernelGGL((product_tile_kernel<EL, NK, MK, BN, BM, WN>), dim3(product_grid(tiles, 512)),
                      dim3(256), 0, st, p);
   return hipGetLastError();
+}
+
+template <int EL, int NK, int MK, int BN, int BM, int WN, int WM, int NSN, int NSM>
+hipError_t launch_big(const ProductArgs& p, long long tiles, hipStream_t st) {
+  hipLaunchKernelGGL((product_big_kernel<EL, NK, MK, BN, BM, WN, WM, NSN, NSM>),
+                     dim3(product_grid(tiles, 256)), dim3(64 * WN * WM), 0, st, p);
+  return hipGetLastError();
+}
+
+// M tiles of bm rows that R rows over E experts can need
+long long row_tiles(const ProductArgs& p, int bm) {
+  return (long long)(p.R / bm) + (p.E < p.R ? p.E : p.R);
+}
+
+// what the large tile's direct loads need: rows at 16-byte steps, a sum (16-bit types) and
+// contiguous columns of whole 16-byte chunks, and gathered rows within 32-bit offsets
+template <int NK>
+bool big_rows_ok(const ProductArgs& p) {
+  if (p.m_pitch % 16 || p.n_pitch % 16) return false;
+  if (NK != kOpPanel && p.K % 8) return false;
+  if (NK == kOpKs && p.N % 8) return false;
+  return !p.row_src || (unsigned long long)p.src_rows * p.m_pitch < (1ull << 32);
 }
 
 template <int EL, int NK>
 hipError_t launch_rows(ProductArgs& p, hipStream_t st) {
   const long long rpe = (p.R + p.E - 1) / p.E;
+  if (rpe > 64 && p.N >= 256 && big_rows_ok<NK>(p)) {
+    const int bm = rpe >= 224 ? 256 : 128, nt = (p.N + 255) / 256;
+    p.band_gm = band_groups_for(nt, bm, rpe);
+    if (bm == 256) return launch_big<EL, NK, kOpKc, 256, 256, 2, 2, 3, 2>(p, row_tiles(p, bm) * nt, st);
+    return launch_big<EL, NK, kOpKc, 256, 128, 2, 2, 3, 3>(p, row_tiles(p, bm) * nt, st);
+  }
   const int bm = rpe <= 32 ? 32 : (rpe <= 64 ? 64 : 128);
   const int nt = (p.N + 127) / 128;
-  const long long mt = (long long)(p.R / bm) + (p.E < p.R ? p.E : p.R);
   p.band_gm = band_groups_for(nt, bm, rpe);
-  if (bm == 32) return launch_tile<EL, NK, kOpKc, 128, 32, 4>(p, mt * nt, st);
-  if (bm == 64) return launch_tile<EL, NK, kOpKc, 128, 64, 2>(p, mt * nt, st);
-  return launch_tile<EL, NK, kOpKc, 128, 128, 2>(p, mt * nt, st);
+  const long long tiles = row_tiles(p, bm) * nt;
+  if (bm == 32) return launch_tile<EL, NK, kOpKc, 128, 32, 4>(p, tiles, st);
+  if (bm == 64) return launch_tile<EL, NK, kOpKc, 128, 64, 2>(p, tiles, st);
+  return launch_tile<EL, NK, kOpKc, 128, 128, 2>(p, tiles, st);
+}
+
+template <int EL>
+hipError_t launch_wgrad(ProductArgs& p, hipStream_t st) {
+  if (p.m_pitch % 16 == 0 && p.n_pitch % 16 == 0 && p.M % 8 == 0 && p.N % 8 == 0 && !p.row_src &&
+      p.M >= 256 && p.N >= 256) {
+    const int nt = (p.N + 255) / 256, mt = (p.M + 255) / 256;
+    p.band_gm = band_groups_for(nt, 256, p.M);
+    return launch_big<EL, kOpKs, kOpKs, 256, 256, 2, 2, 3, 2>(p, (long long)mt * nt * p.E, st);
+  }
+  const int nt = (p.N + 127) / 128, mt = (p.M + 127) / 128;
+  p.band_gm = band_groups_for(nt, 128, p.M);
+  return launch_tile<EL, kOpKs, kOpKs, 128, 128, 2>(p, (long long)mt * nt * p.E, st);
 }
 
 }  // namespace
@@ -245,9 +300,7 @@ hipError_t launch_grouped_gemm(ProductArgs p, int el, bool trans_w, hipStream_t 
 }
 
 hipError_t launch_grouped_wgrad(ProductArgs p, int el, hipStream_t st) {
-  const long long tiles = (long long)((p.M + 127) / 128) * ((p.N + 127) / 128) * p.E;
-  if (el == kPeBf16) return launch_tile<kPeBf16, kOpKs, kOpKs, 128, 128, 2>(p, tiles, st);
-  return launch_tile<kPeFp16, kOpKs, kOpKs, 128, 128, 2>(p, tiles, st);
+  return el == kPeBf16 ? launch_wgrad<kPeBf16>(p, st) : launch_wgrad<kPeFp16>(p, st);
 }
 
 hipError_t launch_int8_gemm(ProductArgs p, hipStream_t st) {
