@@ -149,24 +149,38 @@ __device__ __forceinline__ int fragment_base(int r0, int lane) {
   }
 }
 
+// the lane's place of fragment i within a stage (step 0)
+template <int KIND>
+__device__ __forceinline__ int fragment_place(int base, int i) {
+  // (strided: slot i only touches address bits that the slot of r0 leaves zero)
+  return KIND == kOpKs ? base ^ (i << 5) : base + i * 2048;
+}
+
+// fragment at `place` of the stage, step t (`off`: a constant byte offset)
 template <int KIND, int ROWS>
-__device__ __forceinline__ u32x4_t read_fragment(const uint8_t* stage, int base, int i, int t) {
+__device__ __forceinline__ u32x4_t read_place(const uint8_t* stage, int place, int t,
+                                              int off = 0) {
 #if defined(__HIP_DEVICE_COMPILE__)
   if constexpr (KIND == kOpKs) {
-    // (slot i only touches address bits that the slot of r0 leaves zero)
-    const uint8_t* p0 = stage + (base ^ (i << 5)) + t * (32 * ROWS * 2);
+    const uint8_t* p0 = stage + place + t * (32 * ROWS * 2);
     const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)p0);
     const s16x4_t b =
         __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p0 + 4 * (ROWS * 2)));
     const s16x8_t v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     return __builtin_bit_cast(u32x4_t, v);
   } else {
-    return *reinterpret_cast<const u32x4_t*>(stage + (base ^ (t << 6)) + i * 2048);
+    return *reinterpret_cast<const u32x4_t*>(stage + (place ^ (t << 6)) + off);
   }
 #else
-  (void)stage, (void)base, (void)i, (void)t;
+  (void)stage, (void)place, (void)t, (void)off;
   return u32x4_t{};
 #endif
+}
+
+template <int KIND, int ROWS>
+__device__ __forceinline__ u32x4_t read_fragment(const uint8_t* stage, int base, int i, int t) {
+  if constexpr (KIND == kOpKs) return read_place<KIND, ROWS>(stage, fragment_place<KIND>(base, i), t);
+  else return read_place<KIND, ROWS>(stage, base, t, i * 2048);
 }
 
 // 16 bytes at p of which the first `valid` elements (EB bytes each) exist; the rest are zero

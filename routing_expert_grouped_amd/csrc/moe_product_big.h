@@ -251,11 +251,38 @@ struct ProductBig {
     for (int i = 0; i < NI * NJ; ++i) acc_pin(acc[i / NJ][i % NJ]);
     acc_settle();
 
+    // Lane addresses of the fragments: one per operand where the fragments are constant offsets
+    // apart, one per fragment in registers where they are not (computing them again for every read
+    // costs a wave issue slots that its MFMAs need).
     const int nfrag = fragment_base<NK, BN>(wn * TN, lane);
     const int mfrag = fragment_base<MK, BM>(wm * TM, lane);
+    int nplace[NI], mplace[NJ];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) nplace[i] = fragment_place<NK>(nfrag, i);
+#pragma unroll
+    for (int i = 0; i < NJ; ++i) mplace[i] = fragment_place<MK>(mfrag, i);
+    // fragment i of a step in the order of first use: a[0], every b, the other a
     auto read_one = [&](Frags& f, const uint8_t* ns, const uint8_t* ms, int t, int i) {
-      if (i < NI) f.a[i] = read_fragment<NK, BN>(ns, nfrag, i, t);
-      else f.b[i - NI] = read_fragment<MK, BM>(ms, mfrag, i - NI, t);
+      if (i == 0 || i > NJ) {
+        const int q = i == 0 ? 0 : i - NJ;
+        if constexpr (NK == kOpKs) f.a[q] = read_place<NK, BN>(ns, nplace[q], t);
+        else f.a[q] = read_fragment<NK, BN>(ns, nfrag, q, t);
+      } else {
+        if constexpr (MK == kOpKs) f.b[i - 1] = read_place<MK, BM>(ms, mplace[i - 1], t);
+        else f.b[i - 1] = read_fragment<MK, BM>(ms, mfrag, i - 1, t);
+      }
+    };
+    auto pin_places = [&]() {
+#if defined(__HIP_DEVICE_COMPILE__)
+      if constexpr (NK == kOpKs) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) asm volatile("" : "+v"(nplace[i]));
+      }
+      if constexpr (MK == kOpKs) {
+#pragma unroll
+        for (int i = 0; i < NJ; ++i) asm volatile("" : "+v"(mplace[i]));
+      }
+#endif
     };
 
     // Point j: the wait and barrier that make stage j readable, then its loads, m stage j + NSM - 1
@@ -292,7 +319,7 @@ struct ProductBig {
       constexpr int PART = LAST ? 0 : 1;                // part of the point's loads sent here
       constexpr int D0 = PART * U / 2, ND = S ? (PART + 1) * U / 2 - D0 : 0;
       constexpr int OPS = NR + ND;
-      constexpr int SLOTS = NM - NM / 8;                // (the last MFMAs cover the last reads)
+      constexpr int SLOTS = NM * 3 / 4;                // (the last MFMAs cover the last reads)
       const bool more = !LAST || j + 1 < stages;        // (STEADY: always)
       const uint8_t* ns = lds + nslot(LAST ? j + 1 : j);
       const uint8_t* ms = lds + mslot(LAST ? j + 1 : j);
@@ -349,7 +376,10 @@ struct ProductBig {
 #pragma unroll
       for (int i = 0; i < NR; ++i) read_one(f0, lds + nslot(0), lds + mslot(0), 0, i);
       int j = 0;
-      for (; j + NSN < whole; ++j) stage(j, std::true_type{}, f0, f1);
+      for (; j + NSN < whole; ++j) {
+        pin_places();
+        stage(j, std::true_type{}, f0, f1);
+      }
       for (; j < stages; ++j) stage(j, std::false_type{}, f0, f1);
     }
     lds_barrier();  // every fragment is read: LDS is free for the epilogue

@@ -264,7 +264,7 @@ template <int EL, int NK>
 hipError_t launch_rows(ProductArgs& p, hipStream_t st) {
   const long long rpe = (p.R + p.E - 1) / p.E;
   if (rpe > 64 && p.N >= 256 && big_rows_ok<NK>(p)) {
-    const int bm = rpe >= 224 ? 256 : 128, nt = (p.N + 255) / 256;
+    const int bm = rpe >= 384 ? 256 : 128, nt = (p.N + 255) / 256;
     p.band_gm = band_groups_for(nt, bm, rpe);
     if (bm == 256) return launch_big<EL, NK, kOpKc, 256, 256, 2, 2, 3, 2>(p, row_tiles(p, bm) * nt, st);
     return launch_big<EL, NK, kOpKc, 256, 128, 2, 2, 3, 3>(p, row_tiles(p, bm) * nt, st);
