@@ -110,8 +110,36 @@ __global__ __launch_bounds__(row_block(TPR)) void norm_kernel(NormArgs a) {
 //   dres = a G;   dn = G w gate tau;   dy = r (dn - n mean(dn n));   dtau = sum G n w gate
 // and over the tokens: dw_next = sum dz n';  A = sum G n tau, dw = A gate, dgate = A w.
 // A workgroup keeps its rows' column sums in registers (rows b, b + groups, ...) and writes them
-// as one float32 partial row per sum; norm_bwd_reduce_kernel adds the partial rows in order.
-// Two column sums and up to four rows in flight bound the registers, not the memory.
+// as one float32 partial row per sum; norm_bwd_reduce_kernel adds the partial rows in order. All of
+// a row's loads go out before its first reduction, and the row stays in its 16-bit form between
+// the passes over it (unpacked again in each, which costs nothing next to the loads), so the
+// registers hold two column sums, the row and the three weights (rows wider than 8192 read the
+// weights again for every row: they would not fit beside the rest).
+template <bool FP16, int V>
+struct PackedRow {
+  u32x4_t v[V];
+  __device__ __forceinline__ void load(const uint16_t* row, int t, int tpr, int h) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = row_load(row, t + tpr * i, h);
+  }
+  __device__ __forceinline__ void load_or_one(const uint16_t* row, int t, int tpr, int h) {
+    if (row) {
+      load(row, t, tpr, h);
+    } else {
+      const uint32_t one = FP16 ? 0x3c003c00u : 0x3f803f80u;
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = u32x4_t{one, one, one, one};
+    }
+  }
+  // chunk i as float32; the empty assembly keeps an earlier unpacking from being held instead
+  __device__ __forceinline__ void get(int i, float (&f)[8]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+v"(v[i]));
+#endif
+    unpack8<FP16>(v[i], f);
+  }
+};
+
 template <bool FP16, int TPR, int V, bool POST, bool NEXT>
 __global__ __launch_bounds__(row_block(TPR)) void norm_backward_kernel(NormBwdArgs a, int groups) {
   __shared__ float red[8];
@@ -121,6 +149,13 @@ __global__ __launch_bounds__(row_block(TPR)) void norm_backward_kernel(NormBwdAr
   if (TPR <= 64 && group >= groups) return;
   const int h = a.h;
   const float inv_h = 1.0f / (float)h;
+  constexpr bool HOLD = TPR <= 256;
+  PackedRow<FP16, V> w, gate, wn;
+  if constexpr (POST && HOLD) {
+    w.load_or_one(a.w, t, TPR, h);
+    gate.load_or_one(a.gate, t, TPR, h);
+  }
+  if constexpr (NEXT && HOLD) wn.load_or_one(a.w_next, t, TPR, h);
   float ca[V][8], cz[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v)
@@ -128,41 +163,51 @@ __global__ __launch_bounds__(row_block(TPR)) void norm_backward_kernel(NormBwdAr
     for (int q = 0; q < 8; ++q) ca[v][q] = cz[v][q] = 0.0f;
   for (int row = group; row < a.T; row += groups) {
     const size_t at = (size_t)row * h;
-    float g[V][8];
+    PackedRow<FP16, V> du, dz, u, y;
+    if (a.du) {
+      du.load(a.du + at, t, TPR, h);
+    } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (a.du) {
-        unpack8<FP16>(row_load(a.du + at, t + TPR * v, h), g[v]);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) g[v][q] = 0.0f;
-      }
+      for (int v = 0; v < V; ++v) du.v[v] = u32x4_t{0u, 0u, 0u, 0u};
     }
     if constexpr (NEXT) {
+      dz.load(a.dz + at, t, TPR, h);
+      u.load(a.u + at, t, TPR, h);
+    }
+    if constexpr (POST) y.load(a.y + at, t, TPR, h);
+    float g[V][8];
+    if constexpr (NEXT) {
+      if constexpr (!HOLD) wn.load_or_one(a.w_next, t, TPR, h);
       const float r = a.rstd_next[row];
       float s = 0.0f;
-      float n[V][8], qv[V][8];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int c = t + TPR * v;
-        float w[8];
-        unpack8<FP16>(row_load(a.u + at, c, h), n[v]);
-        unpack8<FP16>(row_load(a.dz + at, c, h), qv[v]);
-        load_vec_or_one<FP16>(a.w_next, c, h, w);
+        float n[8], q[8], wf[8];
+        u.get(v, n);
+        dz.get(v, q);
+        wn.get(v, wf);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          n[v][q] *= r;
-          cz[v][q] = __builtin_fmaf(qv[v][q], n[v][q], cz[v][q]);
-          qv[v][q] *= w[q];
-          s = __builtin_fmaf(qv[v][q], n[v][q], s);
+        for (int i = 0; i < 8; ++i) {
+          n[i] *= r;
+          cz[v][i] = __builtin_fmaf(q[i], n[i], cz[v][i]);
+          s = __builtin_fmaf(q[i] * wf[i], n[i], s);
         }
       }
       const float mean = row_sum<TPR>(s, red) * inv_h;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
+      for (int v = 0; v < V; ++v) {
+        float n[8], q[8], wf[8];
+        u.get(v, n);
+        dz.get(v, q);
+        wn.get(v, wf);
+        du.get(v, g[v]);
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          g[v][q] = __builtin_fmaf(r, __builtin_fmaf(-mean, n[v][q], qv[v][q]), g[v][q]);
+        for (int i = 0; i < 8; ++i)
+          g[v][i] = __builtin_fmaf(r, __builtin_fmaf(-mean, n[i] * r, q[i] * wf[i]), g[v][i]);
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) du.get(v, g[v]);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -172,22 +217,24 @@ __global__ __launch_bounds__(row_block(TPR)) void norm_backward_kernel(NormBwdAr
       row_store(a.dres + at, t + TPR * v, h, pack8<FP16>(o));
     }
     if constexpr (POST) {
+      if constexpr (!HOLD) {
+        w.load_or_one(a.w, t, TPR, h);
+        gate.load_or_one(a.gate, t, TPR, h);
+      }
       const float r = a.rstd[row], tau = a.tau ? a.tau[row] : 1.0f;
       float s = 0.0f;
-      float n[V][8];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int c = t + TPR * v;
-        float w[8], gt[8];
-        unpack8<FP16>(row_load(a.y + at, c, h), n[v]);
-        load_vec_or_one<FP16>(a.w, c, h, w);
-        load_vec_or_one<FP16>(a.gate, c, h, gt);
+        float n[8], wf[8], gf[8];
+        y.get(v, n);
+        w.get(v, wf);
+        gate.get(v, gf);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          n[v][q] *= r;
-          ca[v][q] = __builtin_fmaf(g[v][q] * n[v][q], tau, ca[v][q]);
-          g[v][q] *= w[q] * gt[q];  // dn / tau from here on
-          s = __builtin_fmaf(g[v][q], n[v][q], s);
+          n[q] *= r;
+          ca[v][q] = __builtin_fmaf(g[v][q] * n[q], tau, ca[v][q]);
+          g[v][q] *= wf[q] * gf[q];  // dn / tau from here on
+          s = __builtin_fmaf(g[v][q], n[q], s);
         }
       }
       s = row_sum<TPR>(s, red);
@@ -195,9 +242,10 @@ __global__ __launch_bounds__(row_block(TPR)) void norm_backward_kernel(NormBwdAr
       const float mean = s * inv_h, rt = r * tau;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float o[8];
+        float n[8], o[8];
+        y.get(v, n);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) o[q] = rt * __builtin_fmaf(-mean, n[v][q], g[v][q]);
+        for (int q = 0; q < 8; ++q) o[q] = rt * __builtin_fmaf(-mean, n[q] * r, g[v][q]);
         row_store(a.dy + at, t + TPR * v, h, pack8<FP16>(o));
       }
     }
@@ -216,23 +264,36 @@ __global__ __launch_bounds__(row_block(TPR)) void norm_backward_kernel(NormBwdAr
   }
 }
 
-// column sums of the partial rows: 64 columns per workgroup, four threads per column each adding
-// every fourth partial row in order in 64 bits, then the four in order
+// Column sums of the partial rows: 64 columns per workgroup, 16 threads per column (one wave each)
+// adding every 16th partial row in order in 64 bits, then the 16 sums in order. Sixteen short
+// chains of loads per column instead of one: with four, the 512 partial rows of a 4096-token batch
+// took 32 us, most of it latency.
 template <bool FP16>
-__global__ __launch_bounds__(256) void norm_bwd_reduce_kernel(NormBwdArgs a, int groups,
-                                                              int first) {
-  __shared__ double part[4][64];
+__global__ __launch_bounds__(1024) void norm_bwd_reduce_kernel(NormBwdArgs a, int groups,
+                                                               int first) {
+  __shared__ double part[16][64];
   const int cx = threadIdx.x & 63, gy = threadIdx.x >> 6;
   const int col = blockIdx.x * 64 + cx;
   const bool next = blockIdx.y + first == 1;
-  const float* p = a.partial + (next ? (size_t)groups * a.h : 0);
+  const float* p = a.partial + (next ? (size_t)groups * a.h : 0) + col;
   double s = 0.0;
-  if (col < a.h)
-    for (int g = gy; g < groups; g += 4) s += (double)p[(size_t)g * a.h + col];
+  if (col < a.h) {
+    int g = gy;
+    for (; g + 7 * 16 < groups; g += 8 * 16) {
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = p[(size_t)(g + 16 * q) * a.h];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s += (double)v[q];
+    }
+    for (; g < groups; g += 16) s += (double)p[(size_t)g * a.h];
+  }
   part[gy][cx] = s;
   __syncthreads();
   if (gy != 0 || col >= a.h) return;
-  s = part[0][cx] + part[1][cx] + part[2][cx] + part[3][cx];
+  s = 0.0;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) s += part[q][cx];
   auto vec = [&](const uint16_t* w) -> double {
     if (!w) return 1.0;
     if constexpr (FP16) return (double)(float)__builtin_bit_cast(_Float16, w[col]);
@@ -296,9 +357,9 @@ hipError_t launch_norm_backward(const NormBwdArgs& a, bool post, bool next, bool
     const dim3 g((a.h + 63) / 64, want_a && want_z ? 2 : 1);
     const int first = want_a ? 0 : 1;
     if (fp16)
-      hipLaunchKernelGGL((norm_bwd_reduce_kernel<true>), g, dim3(256), 0, st, a, groups, first);
+      hipLaunchKernelGGL((norm_bwd_reduce_kernel<true>), g, dim3(1024), 0, st, a, groups, first);
     else
-      hipLaunchKernelGGL((norm_bwd_reduce_kernel<false>), g, dim3(256), 0, st, a, groups, first);
+      hipLaunchKernelGGL((norm_bwd_reduce_kernel<false>), g, dim3(1024), 0, st, a, groups, first);
   }
   return hipGetLastError();
 }
