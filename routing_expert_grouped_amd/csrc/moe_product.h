@@ -11,6 +11,8 @@
 //   int8                 : m = code rows, n = packed weight panels, both contiguous
 #pragma once
 
+#include <type_traits>
+
 #include "moe_internal.h"
 #include "moe_tile_order.h"
 
@@ -346,5 +348,7 @@ namespace moe {
 hipError_t launch_grouped_gemm(ProductArgs p, int el, bool trans_w, hipStream_t st);
 hipError_t launch_grouped_wgrad(ProductArgs p, int el, hipStream_t st);
 hipError_t launch_int8_gemm(ProductArgs p, hipStream_t st);
+// the few-row form (moe_int8_few_kernels.hip), `rows` the rows per expert on average
+hipError_t launch_int8_few(ProductArgs p, int rows, hipStream_t st);
 
 }  // namespace moe

@@ -103,6 +103,68 @@ __device__ __forceinline__ void acc_pin(Acc& c) {  // c is in its accumulator re
 #endif
 }
 
+// ------------------------------------------------------------------------------------------------
+// M tiles without LDS (the rings may fill it): every wave holds the first tile of up to 16 experts
+// per lane and finds a tile's expert by ballots.
+// ------------------------------------------------------------------------------------------------
+struct WaveTiles {
+  int epl;    // experts per lane
+  int first;  // tiles before expert lane * epl
+  int total;
+};
+
+__device__ __forceinline__ WaveTiles wave_tiles(const ProductArgs& p, int bm) {
+  WaveTiles x;
+  const int lane = threadIdx.x & 63;
+  x.epl = (p.E + 63) / 64;
+  int cnt = 0;
+  for (int q = 0; q < x.epl; ++q) {
+    const int e = lane * x.epl + q;
+    if (e < p.E) {
+      int lo, hi;
+      expert_rows(p, e, lo, hi);
+      cnt += (hi - lo + bm - 1) / bm;
+    }
+  }
+  int inc = cnt;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(inc, d);
+    if (lane >= d) inc += o;
+  }
+  x.first = inc - cnt;
+  x.total = __builtin_amdgcn_readlane(inc, 63);
+  return x;
+}
+
+struct TileAt {
+  int e, row0, row_end, n0;
+};
+
+// expert and rows of M tile ti (< total), uniform: the last lane whose experts start at or before
+// ti holds it, and of that lane's experts (one per lane now) again the last
+__device__ __forceinline__ void wave_lookup(const ProductArgs& p, const WaveTiles& x, int ti,
+                                            int bm, TileAt& at) {
+  const int lane = threadIdx.x & 63;
+  const int sel = 63 - __builtin_clzll(__ballot(x.first <= ti));
+  const int e = sel * x.epl + lane;
+  const bool mine = lane < x.epl && e < p.E;
+  int lo = 0, hi = 0;
+  if (mine) expert_rows(p, e, lo, hi);
+  const int cnt = (hi - lo + bm - 1) / bm;
+  int inc = cnt;
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) {
+    const int o = __shfl_up(inc, d);
+    if (lane >= d) inc += o;
+  }
+  const int start = __builtin_amdgcn_readlane(x.first, sel) + inc - cnt;
+  const int pick = 63 - __builtin_clzll(__ballot(mine && start <= ti));
+  at.e = sel * x.epl + pick;
+  at.row0 = __builtin_amdgcn_readlane(lo, pick) + (ti - __builtin_amdgcn_readlane(start, pick)) * bm;
+  at.row_end = __builtin_amdgcn_readlane(hi, pick);
+}
+
 template <int EL, int NK, int MK, int BN, int BM, int WN, int WM, int NSN, int NSM>
 struct ProductBig {
   static constexpr int kWaves = WN * WM;
@@ -115,17 +177,13 @@ struct ProductBig {
   static constexpr int BK = 128 / EB;
   static constexpr int kNStage = BN * 128, kMStage = BM * 128;
   static constexpr bool kWgrad = MK == kOpKs;
-  // epilogue: a wave's 32 rows x TN columns of float32, rows padded by 16 bytes
-  static constexpr int kEpiPitch = TN * 4 + 16;
-  static constexpr int kEpi = kWaves * 32 * kEpiPitch;
-  static constexpr int kRings = NSN * kNStage + NSM * kMStage;
-  static constexpr int kLds = kRings > kEpi ? kRings : kEpi;
+  static constexpr int kLds = NSN * kNStage + NSM * kMStage;
   // loads that may be in flight at a point: those issued after the stage it waits for. A point
   // issues its m stage, then its n stage.
-  static constexpr int kFlying = (NSM == 3 ? MQ : 0) + (NSN == 3 ? NQ : 0);
+  static constexpr int kFlying = NSM == NSN ? (MQ + NQ) * (NSN - 2) : NQ;
   static_assert(kLds <= 160 * 1024, "LDS budget");
   static_assert(NQ * kThreads == BN * 8 && MQ * kThreads == BM * 8, "whole chunks");
-  static_assert((NSN == 2 || NSN == 3) && (NSM == 2 || (NSM == 3 && NSN == 3)), "ring depths");
+  static_assert(NSN >= 2 && (NSM == NSN || (NSM == 2 && NSN == 3)), "ring depths");
   static_assert(kFlying < 64, "vmcnt range");
   using Acc = typename ProductTypes<EL>::Acc;
 
@@ -148,108 +206,111 @@ struct ProductBig {
     u32x4_t a[NI], b[NJ];
   };
 
-  static __device__ __forceinline__ void run(const ProductArgs& p, int e, int row0, int row_end,
-                                             int n0, uint8_t* lds) {
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wn = wave / WM, wm = wave % WM;
-    int k_lo = 0, k_hi = p.K;
-    if constexpr (kWgrad) expert_rows(p, e, k_lo, k_hi);
-    const int klen = __builtin_amdgcn_readfirstlane(k_hi - k_lo);
-    const int whole = klen / BK;
-    const bool part = klen % BK != 0;
-    const int stages = whole + (part ? 1 : 0);
+  // where a tile's operands lie: uniform bases, per-lane byte offsets, bytes and count of stages
+  struct Source {
+    const uint8_t *nb, *mb;
+    size_t nstep, mstep;
+    uint32_t noff[NQ], moff[MQ];
+    int whole, stages, left;  // whole stages, all stages, elements of the partial one
+  };
 
-    // uniform operand bases of the tile, per-lane byte offsets from them, bytes per stage
-    const uint8_t* nb = p.n_base + (size_t)e * p.n_estride;
-    size_t nstep;
-    uint32_t noff[NQ];
+  static __device__ __forceinline__ void set_source(const ProductArgs& p, const TileAt& at,
+                                                    Source& s) {
+    const int tid = threadIdx.x;
+    int k_lo = 0, k_hi = p.K;
+    if constexpr (kWgrad) expert_rows(p, at.e, k_lo, k_hi);
+    const int klen = __builtin_amdgcn_readfirstlane(k_hi - k_lo);
+    s.whole = klen / BK;
+    s.left = klen - s.whole * BK;
+    s.stages = s.whole + (s.left ? 1 : 0);
+    const uint8_t* nb = p.n_base + (size_t)at.e * p.n_estride;
     if constexpr (NK == kOpKs) {
-      nb += (size_t)k_lo * p.n_pitch + (size_t)n0 * EB;
-      nstep = (size_t)BK * p.n_pitch;
+      nb += (size_t)k_lo * p.n_pitch + (size_t)at.n0 * EB;
+      s.nstep = (size_t)BK * p.n_pitch;
     } else if constexpr (NK == kOpPanel) {
-      nb += (size_t)(n0 >> 4) * p.n_pitch;
-      nstep = 2048;
+      nb += (size_t)(at.n0 >> 4) * p.n_pitch;
+      s.nstep = 2048;
     } else {
-      nb += (size_t)n0 * p.n_pitch;
-      nstep = 128;
+      nb += (size_t)at.n0 * p.n_pitch;
+      s.nstep = 128;
     }
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
       int row, c;
       chunk_of<NK, BN>(q * kThreads + tid, row, c);
       if constexpr (NK == kOpKs) {
-        noff[q] = (uint32_t)(row * (int)p.n_pitch + min(8 * c, p.N - n0 - 8) * EB);
+        s.noff[q] = (uint32_t)(row * (int)p.n_pitch + min(8 * c, p.N - at.n0 - 8) * EB);
       } else {
-        const int r = min(row, p.N - 1 - n0);
+        const int r = min(row, p.N - 1 - at.n0);
         if constexpr (NK == kOpPanel)
-          noff[q] = (uint32_t)((r >> 4) * (int)p.n_pitch + (r & 15) * 128 + 16 * c);
+          s.noff[q] = (uint32_t)((r >> 4) * (int)p.n_pitch + (r & 15) * 128 + 16 * c);
         else
-          noff[q] = (uint32_t)(r * (int)p.n_pitch + 16 * c);
+          s.noff[q] = (uint32_t)(r * (int)p.n_pitch + 16 * c);
       }
     }
     const uint8_t* mb = p.m_base;
-    size_t mstep = 128;
-    uint32_t moff[MQ];
+    s.mstep = 128;
     if constexpr (kWgrad) {
-      mb += (size_t)k_lo * p.m_pitch + (size_t)row0 * EB;
-      mstep = (size_t)BK * p.m_pitch;
+      mb += (size_t)k_lo * p.m_pitch + (size_t)at.row0 * EB;
+      s.mstep = (size_t)BK * p.m_pitch;
     } else if (!p.row_src) {
-      mb += (size_t)row0 * p.m_pitch;
+      mb += (size_t)at.row0 * p.m_pitch;
     }
 #pragma unroll
     for (int q = 0; q < MQ; ++q) {
       int row, c;
       chunk_of<MK, BM>(q * kThreads + tid, row, c);
       if constexpr (kWgrad) {
-        moff[q] = (uint32_t)(row * (int)p.m_pitch + min(8 * c, p.M - row0 - 8) * EB);
+        s.moff[q] = (uint32_t)(row * (int)p.m_pitch + min(8 * c, p.M - at.row0 - 8) * EB);
       } else {
-        const int r = min(row0 + row, row_end - 1);
-        moff[q] = (uint32_t)((p.row_src ? source_row(p, r) : r - row0) * (uint32_t)p.m_pitch +
-                             16 * c);
+        const int r = min(at.row0 + row, at.row_end - 1);
+        s.moff[q] = (uint32_t)((p.row_src ? source_row(p, r) : r - at.row0) *
+                                   (uint32_t)p.m_pitch + 16 * c);
       }
     }
-    nb = uniform_ptr(nb);
-    mb = uniform_ptr(mb);
+    s.nb = uniform_ptr(nb);
+    s.mb = uniform_ptr(mb);
+  }
+
+  // Every tile of the calling workgroup. `next(at)` gives its tiles in turn (false: no more). The
+  // loads of a tile's first stages go out before the stores of the tile before it.
+  template <class Next>
+  static __device__ __forceinline__ void run(const ProductArgs& p, uint8_t* lds, Next next) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave / WM, wm = wave % WM;
+    TileAt at;
+    if (!next(at)) return;
+    Source s;
 
     const uint32_t ring = __builtin_amdgcn_readfirstlane(lds_address(lds));
     auto nslot = [&](int j) { return (j % NSN) * kNStage; };
     auto mslot = [&](int j) { return NSN * kNStage + (j % NSM) * kMStage; };
     auto load_n = [&](int j, int q) {
-      dma16_at(nb + (size_t)j * nstep, noff[q], ring + nslot(j) + (q * kWaves + wave) * 1024);
+      dma16_at(s.nb + (size_t)j * s.nstep, s.noff[q],
+               ring + nslot(j) + (q * kWaves + wave) * 1024);
     };
     auto load_m = [&](int j, int q) {
-      dma16_at(mb + (size_t)j * mstep, moff[q], ring + mslot(j) + (q * kWaves + wave) * 1024);
+      dma16_at(s.mb + (size_t)j * s.mstep, s.moff[q],
+               ring + mslot(j) + (q * kWaves + wave) * 1024);
     };
     // the same for a stage that may be the partial one (chunks are whole or absent)
-    const int left = klen - whole * BK;
     auto load_n_any = [&](int j, int q) {
       int row, c;
       chunk_of<NK, BN>(q * kThreads + tid, row, c);
-      const bool there = j < whole || NK == kOpPanel ||
-                         (NK == kOpKs ? row < left : c * (16 / EB) < left);
-      dma16_from(there ? nb + (size_t)j * nstep + noff[q] : kZeroChunk,
+      const bool there = j < s.whole || NK == kOpPanel ||
+                         (NK == kOpKs ? row < s.left : c * (16 / EB) < s.left);
+      dma16_from(there ? s.nb + (size_t)j * s.nstep + s.noff[q] : kZeroChunk,
                  ring + nslot(j) + (q * kWaves + wave) * 1024);
     };
     auto load_m_any = [&](int j, int q) {
       int row, c;
       chunk_of<MK, BM>(q * kThreads + tid, row, c);
-      const bool there = j < whole || EL == kPeI8 ||
-                         (MK == kOpKs ? row < left : c * (16 / EB) < left);
-      dma16_from(there ? mb + (size_t)j * mstep + moff[q] : kZeroChunk,
+      const bool there = j < s.whole || EL == kPeI8 ||
+                         (MK == kOpKs ? row < s.left : c * (16 / EB) < s.left);
+      dma16_from(there ? s.mb + (size_t)j * s.mstep + s.moff[q] : kZeroChunk,
                  ring + mslot(j) + (q * kWaves + wave) * 1024);
     };
-
-    Acc acc[NI][NJ];
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][j][q] = 0;
-#pragma unroll
-    for (int i = 0; i < NI * NJ; ++i) acc_pin(acc[i / NJ][i % NJ]);
-    acc_settle();
 
     // Lane addresses of the fragments: one per operand where the fragments are constant offsets
     // apart, one per fragment in registers where they are not (computing them again for every read
@@ -297,18 +358,36 @@ struct ProductBig {
 #pragma unroll
       for (int u = part * U / 2; u < (part + 1) * U / 2; ++u) {
         if (u < MQ) {
-          if (j + NSM - 1 < stages) load_m_any(j + NSM - 1, u);
+          if (j + NSM - 1 < s.stages) load_m_any(j + NSM - 1, u);
         } else {
-          if (j + NSN - 1 < stages) load_n_any(j + NSN - 1, u - MQ);
+          if (j + NSN - 1 < s.stages) load_n_any(j + NSN - 1, u - MQ);
         }
       }
     };
+    // (with NSM = 2, NSN = 3 the loads behind stage j's are those of n stage j + 1; with equal
+    // depths those of stages j + 1 .. j + NSN - 2; where some of them do not exist, all are waited
+    // for)
     auto point = [&](int j) {
-      if (j + 1 < stages) wait_vmcnt_fenced<kFlying>();
+      constexpr int LAST = NSM == NSN ? NSN - 2 : 1;
+      if (j + LAST < s.stages) wait_vmcnt_fenced<kFlying>();
       else wait_vmcnt_fenced<0>();
       lds_barrier();
     };
+    auto prologue = [&]() {  // the points before 0
+#pragma unroll
+      for (int j = 1 - NSN; j < 0; ++j) {
+        if (j + NSM - 1 >= 0 && j + NSM - 1 < s.stages) {
+#pragma unroll
+          for (int q = 0; q < MQ; ++q) load_m_any(j + NSM - 1, q);
+        }
+        if (j + NSN - 1 < s.stages) {
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) load_n_any(j + NSN - 1, q);
+        }
+      }
+    };
 
+    Acc acc[NI][NJ];
     // step t of stage j on fragments `cur`: its MFMAs with, between them, the reads of the next
     // step into `nxt` and a part of the loads of the current point
     constexpr int NM = NI * NJ, NR = NI + NJ;
@@ -319,8 +398,8 @@ struct ProductBig {
       constexpr int PART = LAST ? 0 : 1;                // part of the point's loads sent here
       constexpr int D0 = PART * U / 2, ND = S ? (PART + 1) * U / 2 - D0 : 0;
       constexpr int OPS = NR + ND;
-      constexpr int SLOTS = NM * 3 / 4;                // (the last MFMAs cover the last reads)
-      const bool more = !LAST || j + 1 < stages;        // (STEADY: always)
+      constexpr int SLOTS = NM >= 16 ? NM * 3 / 4 : NM; // (the last MFMAs cover the last reads)
+      const bool more = !LAST || j + 1 < s.stages;      // (STEADY: always)
       const uint8_t* ns = lds + nslot(LAST ? j + 1 : j);
       const uint8_t* ms = lds + mslot(LAST ? j + 1 : j);
       const int dj = LAST ? j + 1 : j;                  // whose point's loads go out here
@@ -345,9 +424,9 @@ struct ProductBig {
           if (op < OPS) {
             constexpr int PAIRS = 2 * (ND < NR ? ND : NR);
             const bool load = op < PAIRS ? op % 2 == 1 : ND > NR;
-            const int at = op < PAIRS ? op / 2 : op - PAIRS / 2;
-            if (load) load_unit(dj, D0 + at);
-            else read_one(nxt, ns, ms, LAST ? 0 : t + 1, at);
+            const int k = op < PAIRS ? op / 2 : op - PAIRS / 2;
+            if (load) load_unit(dj, D0 + k);
+            else read_one(nxt, ns, ms, LAST ? 0 : t + 1, k);
           }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -358,86 +437,105 @@ struct ProductBig {
       step(j, std::integral_constant<int, 1>{}, steady, f1, f0);
     };
 
-    if (stages > 0) {
+    set_source(p, at, s);
+    prologue();
+    while (true) {
 #pragma unroll
-      for (int j = 1 - NSN; j < 0; ++j) {  // the points before 0
-        if (j + NSM - 1 >= 0 && j + NSM - 1 < stages) {
+      for (int i = 0; i < NI; ++i)
 #pragma unroll
-          for (int q = 0; q < MQ; ++q) load_m_any(j + NSM - 1, q);
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[i][j][q] = 0;
+#pragma unroll
+      for (int i = 0; i < NM; ++i) acc_pin(acc[i / NJ][i % NJ]);
+      acc_settle();
+      if (s.stages > 0) {
+        Frags f0, f1;
+        point(0);
+        load_part(0, 0);
+#pragma unroll
+        for (int i = 0; i < NR; ++i) read_one(f0, lds + nslot(0), lds + mslot(0), 0, i);
+        int j = 0;
+        for (; j + NSN < s.whole; ++j) {
+          pin_places();
+          stage(j, std::true_type{}, f0, f1);
         }
-        if (j + NSN - 1 < stages) {
-#pragma unroll
-          for (int q = 0; q < NQ; ++q) load_n_any(j + NSN - 1, q);
-        }
+        for (; j < s.stages; ++j) stage(j, std::false_type{}, f0, f1);
       }
-      Frags f0, f1;
-      point(0);
-      load_part(0, 0);
-#pragma unroll
-      for (int i = 0; i < NR; ++i) read_one(f0, lds + nslot(0), lds + mslot(0), 0, i);
-      int j = 0;
-      for (; j + NSN < whole; ++j) {
-        pin_places();
-        stage(j, std::true_type{}, f0, f1);
-      }
-      for (; j < stages; ++j) stage(j, std::false_type{}, f0, f1);
-    }
-    lds_barrier();  // every fragment is read: LDS is free for the epilogue
-    acc_settle();
-#pragma unroll
-    for (int i = 0; i < NI * NJ; ++i) acc_pin(acc[i / NJ][i % NJ]);
-
-    // acc[i][j][q]: column n0 + wn TN + 16 i + 4 (lane / 16) + q,
-    //               row row0 + wm TM + 16 j + lane % 16.
-    // Each wave turns its tile through its own part of LDS, 32 rows at a time, so that a store
-    // instruction writes whole 128-byte lines of a few rows.
-    const int row_lim = kWgrad ? p.M : row_end;
-    uint8_t* w = lds + wave * (32 * kEpiPitch);
-#pragma unroll
-    for (int jj = 0; jj < NJ / 2; ++jj) {
-      const int r0 = row0 + wm * TM + 32 * jj;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int lr = 16 * h + (lane & 15);
-        float ms = 1.0f;
-        if constexpr (EL == kPeI8) ms = p.m_scale[source_row(p, min(r0 + lr, row_end - 1))];
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          f32x4v_t v;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            v[q] = (float)acc[i][2 * jj + h][q];
-            if constexpr (EL == kPeI8) v[q] *= ms;
-          }
-          *reinterpret_cast<f32x4v_t*>(w + lr * kEpiPitch + (16 * i + 4 * (lane >> 4)) * 4) = v;
-        }
-      }
-      // (the wave's own LDS operations stay in order; the compiler waits for the reads)
-      constexpr int LPR = TN / 4, RPI = 64 / LPR;  // lanes per row, rows per instruction
-      const int c4 = (lane % LPR) * 4, n = n0 + wn * TN + c4;
-      f32x4v_t ns = {1.0f, 1.0f, 1.0f, 1.0f}, bs = {0.0f, 0.0f, 0.0f, 0.0f};
+      const TileAt done = at;
+      // int8: the scales of the finished tile, loaded before the next tile's stages
+      float ms[NJ];
+      f32x4v_t sc[NI], bs[NI];
       if constexpr (EL == kPeI8) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const size_t c = (size_t)e * p.N + min(n + q, p.N - 1);
-          ns[q] = p.n_scale[c];
-          if (p.bias) bs[q] = p.bias[c];
+        for (int j = 0; j < NJ; ++j)
+          ms[j] = p.m_scale[source_row(
+              p, min(done.row0 + wm * TM + 16 * j + (lane & 15), done.row_end - 1))];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const size_t c = (size_t)done.e * p.N +
+                           min(done.n0 + wn * TN + 16 * i + 4 * (lane >> 4), p.N - 4);
+          sc[i] = *reinterpret_cast<const f32x4v_t*>(p.n_scale + c);
+          bs[i] = p.bias ? *reinterpret_cast<const f32x4v_t*>(p.bias + c)
+                         : f32x4v_t{0.0f, 0.0f, 0.0f, 0.0f};
         }
+#if defined(__HIP_DEVICE_COMPILE__)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) asm volatile("" : "+v"(ms[j]));
+#pragma unroll
+        for (int i = 0; i < NI; ++i) asm volatile("" : "+v"(sc[i]), "+v"(bs[i]));
+#endif
       }
+      lds_barrier();  // every fragment of the tile is read: its ring slots are free
+      const bool more = next(at);
+      if (more) {
+        set_source(p, at, s);
+        prologue();
+      }
+      // The output, straight from the accumulators: acc[i][j][q] is column
+      // n0 + wn TN + 16 i + 4 (lane / 16) + q of row row0 + wm TM + 16 j + lane % 16, so a store
+      // writes 32 (16-bit) or 64 bytes of 16 rows. A whole tile's stores carry no conditions, and
+      // each row of fragments is only taken out of its accumulators when it is stored.
+      acc_settle();
+      const int row_lim = kWgrad ? p.M : done.row_end;
+      const int n = done.n0 + wn * TN + 4 * (lane >> 4);
+      auto store = [&](auto kind_tag, auto whole_tag) {
+        constexpr int KIND = decltype(kind_tag)::value;
+        constexpr bool WHOLE = decltype(whole_tag)::value;
+        constexpr int ES = KIND == kOutF32 ? 4 : 2;
 #pragma unroll
-      for (int k = 0; k < 32 / RPI; ++k) {
-        const int rr = k * RPI + lane / LPR, r = r0 + rr;
-        f32x4v_t v = *reinterpret_cast<const f32x4v_t*>(w + rr * kEpiPitch + c4 * 4);
-        if constexpr (EL == kPeI8) {
+        for (int j = 0; j < NJ; ++j) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            v[q] *= ns[q];
-            if (p.bias) v[q] += bs[q];
+          for (int i = 0; i < NI; ++i) acc_pin(acc[i][j]);
+          const int r = done.row0 + wm * TM + 16 * j + (lane & 15);
+          if (!WHOLE && r >= row_lim) continue;
+          uint8_t* o = reinterpret_cast<uint8_t*>(p.out) +
+                       (((size_t)r + (kWgrad ? (size_t)done.e * p.M : 0)) * p.out_ld + n) * ES;
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            if (!WHOLE && n + 16 * i >= p.N) continue;
+            f32x4v_t v;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              v[q] = (float)acc[i][j][q];
+              if constexpr (EL == kPeI8) v[q] = v[q] * ms[j] * sc[i][q];
+            }
+            if (EL == kPeI8 && p.bias) v += bs[i];
+            if constexpr (KIND == kOutF32) *reinterpret_cast<f32x4v_t*>(o + 16 * i * ES) = v;
+            else
+              *reinterpret_cast<uint2*>(o + 16 * i * ES) =
+                  KIND == kOutBf16 ? round_bf16x4(v) : round_fp16x4(v);
           }
         }
-        if (r < row_lim && n < p.N)
-          store_run(p, ((size_t)r + (kWgrad ? (size_t)e * p.M : 0)) * p.out_ld + n, n, v);
-      }
+      };
+      auto store_kind = [&](auto whole_tag) {
+        if (p.out_kind == kOutF32) store(std::integral_constant<int, kOutF32>{}, whole_tag);
+        else if (p.out_kind == kOutBf16) store(std::integral_constant<int, kOutBf16>{}, whole_tag);
+        else store(std::integral_constant<int, kOutFp16>{}, whole_tag);
+      };
+      if (done.n0 + BN <= p.N && done.row0 + BM <= row_lim) store_kind(std::true_type{});
+      else store_kind(std::false_type{});
+      if (!more) return;
     }
   }
 };

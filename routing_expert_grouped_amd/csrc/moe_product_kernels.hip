@@ -218,10 +218,33 @@ __global__ __launch_bounds__(256, 2) void product_tile_kernel(ProductArgs p) {
 template <int EL, int NK, int MK, int BN, int BM, int WN, int WM, int NSN, int NSM>
 __global__ __launch_bounds__(64 * WN * WM, WN * WM / 4) void product_big_kernel(ProductArgs p) {
   using Tile = ProductBig<EL, NK, MK, BN, BM, WN, WM, NSN, NSM>;
-  // one LDS object: beside a second one the compiler waits for every direct load before the next
-  // LDS read. The tile lookup's few words share it with the rings, a barrier apart.
   __shared__ __attribute__((aligned(16))) uint8_t lds[Tile::kLds];
-  product_tiles<Tile, BN, BM, WN * WM>(p, lds, reinterpret_cast<int*>(lds));
+  const int nt_total = (p.N + BN - 1) / BN;
+  int jx = blockIdx.x >> 3;
+  const int xcd = blockIdx.x & 7, per = gridDim.x >> 3;
+  if constexpr (Tile::kWgrad) {
+    const int mt = (p.M + BM - 1) / BM;
+    Tile::run(p, lds, [&](TileAt& at) {
+      int ti, nt;
+      if (!big_tile_coords(mt * p.E, nt_total, p.band_gm, xcd, jx, ti, nt)) return false;
+      jx += per;
+      at.e = __builtin_amdgcn_readfirstlane(ti / mt);
+      at.row0 = __builtin_amdgcn_readfirstlane((ti % mt) * BM);
+      at.row_end = p.M;
+      at.n0 = nt * BN;
+      return true;
+    });
+  } else {
+    const WaveTiles x = wave_tiles(p, BM);
+    Tile::run(p, lds, [&](TileAt& at) {
+      int ti, nt;
+      if (!big_tile_coords(x.total, nt_total, p.band_gm, xcd, jx, ti, nt)) return false;
+      jx += per;
+      wave_lookup(p, x, __builtin_amdgcn_readfirstlane(ti), BM, at);
+      at.n0 = __builtin_amdgcn_readfirstlane(nt * BN);
+      return true;
+    });
+  }
 }
 
 // workgroups of a persistent launch: at most `slots` (those that run at once), no more than the
@@ -250,11 +273,13 @@ long long row_tiles(const ProductArgs& p, int bm) {
   return (long long)(p.R / bm) + (p.E < p.R ? p.E : p.R);
 }
 
-// what the large tile's direct loads need: rows at 16-byte steps, a sum (16-bit types) and
-// contiguous columns of whole 16-byte chunks, and gathered rows within 32-bit offsets
+// what the large tile's direct loads and stores need: rows at 16-byte steps, a sum (16-bit types)
+// and contiguous columns of whole 16-byte chunks, gathered rows within 32-bit offsets, and output
+// columns in whole runs of four
 template <int NK>
 bool big_rows_ok(const ProductArgs& p) {
   if (p.m_pitch % 16 || p.n_pitch % 16) return false;
+  if (p.N % 4 || !p.out_vec) return false;
   if (NK != kOpPanel && p.K % 8) return false;
   if (NK == kOpKs && p.N % 8) return false;
   return !p.row_src || (unsigned long long)p.src_rows * p.m_pitch < (1ull << 32);
@@ -304,6 +329,15 @@ hipError_t launch_grouped_wgrad(ProductArgs p, int el, hipStream_t st) {
 }
 
 hipError_t launch_int8_gemm(ProductArgs p, hipStream_t st) {
+  // Too few 128-column tiles to fill the CUs: split the sum over waves instead. The few-row kernel
+  // reads the codes once per 16 columns, so its work grows with rows x columns: measured equal at
+  // rows (each expert's at least 16) x 128-column tiles = 4096 (1 x 128 rows of 7168 x 4096: 37 us
+  // against the tile's 57; 4 x 64 rows: 66 against 49; 8 x 1: 42 against 42), and for short sums,
+  // where a tile's latency is short too, earlier (64 x 2 rows of 512 x 512: 13.5 against 6.4).
+  const long long hit = p.E < p.R ? p.E : p.R, r16 = p.R > 16 * hit ? p.R : 16 * hit;
+  const long long size = r16 * ((p.N + 127) / 128);
+  if (size <= (p.K >= 2048 ? 4096 : 1024))
+    return launch_int8_few(p, (p.R + p.E - 1) / p.E, st);
   return launch_rows<kPeI8, kOpPanel>(p, st);
 }
 
