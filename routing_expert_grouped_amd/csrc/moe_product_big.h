@@ -69,35 +69,12 @@ __device__ __forceinline__ uint32_t lds_address(const uint8_t* l) {
 #endif
 }
 
-// product_mfma with the accumulators held in the accumulator registers: 256 of them per lane are all
-// there are, and left to itself the compiler moves some through vector registers around every
-// MFMA. What the compiler does not see of such an MFMA: its result may be read by another
-// instruction only after the unit's latency (acc_settle below), and a register it reads as
-// accumulator only that long after a vector write.
-template <int EL>
-__device__ __forceinline__ void product_mfma_acc(u32x4_t a, u32x4_t b,
-                                                 typename ProductTypes<EL>::Acc& c) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  if constexpr (EL == kPeBf16)
-    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-  else if constexpr (EL == kPeFp16)
-    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-  else
-    asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-#else
-  (void)a, (void)b, (void)c;
-#endif
-}
-
-// more than the longest MFMA latency (and than the wait before an MFMA reads a written accumulator)
-__device__ __forceinline__ void acc_settle() {
-#if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
-#endif
-}
-
+// c is in accumulator registers here. The tile's 256 sums per lane are all of them; pinned at every
+// step they stay there, while left to itself the compiler moves some through vector registers and
+// scratch around every MFMA. (The MFMAs themselves stay the compiler's: it keeps the waits that
+// reading a result too early would need.)
 template <class Acc>
-__device__ __forceinline__ void acc_pin(Acc& c) {  // c is in its accumulator registers here
+__device__ __forceinline__ void acc_pin(Acc& c) {
 #if defined(__HIP_DEVICE_COMPILE__)
   asm volatile("" : "+a"(c));
 #endif
@@ -403,6 +380,8 @@ struct ProductBig {
       const uint8_t* ns = lds + nslot(LAST ? j + 1 : j);
       const uint8_t* ms = lds + mslot(LAST ? j + 1 : j);
       const int dj = LAST ? j + 1 : j;                  // whose point's loads go out here
+#pragma unroll
+      for (int i = 0; i < NM; ++i) acc_pin(acc[i / NJ][i % NJ]);
       if (!S && !LAST) load_part(j, 1);
       if (!S && LAST && more) {
         point(j + 1);
@@ -410,7 +389,8 @@ struct ProductBig {
       }
 #pragma unroll
       for (int m = 0; m < NM; ++m) {
-        product_mfma_acc<EL>(cur.a[m / NJ], cur.b[m % NJ], acc[m / NJ][m % NJ]);
+        acc[m / NJ][m % NJ] =
+            product_mfma<EL>(cur.a[m / NJ], cur.b[m % NJ], acc[m / NJ][m % NJ]);
         __builtin_amdgcn_sched_barrier(0);
         if (S && LAST && m == 0) {
           wait_vmcnt_fenced<kFlying>();
@@ -448,10 +428,12 @@ struct ProductBig {
           for (int q = 0; q < 4; ++q) acc[i][j][q] = 0;
 #pragma unroll
       for (int i = 0; i < NM; ++i) acc_pin(acc[i / NJ][i % NJ]);
-      acc_settle();
       if (s.stages > 0) {
         Frags f0, f1;
-        point(0);
+        // everything is waited for here, the stores of the tile before included: they were issued
+        // after this tile's first loads, and a count cannot tell which of the two has returned
+        wait_vmcnt_fenced<0>();
+        lds_barrier();
         load_part(0, 0);
 #pragma unroll
         for (int i = 0; i < NR; ++i) read_one(f0, lds + nslot(0), lds + mslot(0), 0, i);
@@ -496,7 +478,6 @@ struct ProductBig {
       // n0 + wn TN + 16 i + 4 (lane / 16) + q of row row0 + wm TM + 16 j + lane % 16, so a store
       // writes 32 (16-bit) or 64 bytes of 16 rows. A whole tile's stores carry no conditions, and
       // each row of fragments is only taken out of its accumulators when it is stored.
-      acc_settle();
       const int row_lim = kWgrad ? p.M : done.row_end;
       const int n = done.n0 + wn * TN + 4 * (lane >> 4);
       auto store = [&](auto kind_tag, auto whole_tag) {
