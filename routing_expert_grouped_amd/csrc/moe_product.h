@@ -200,6 +200,40 @@ __device__ __forceinline__ u32x4_t load_chunk(const uint8_t* p, int valid) {
   return v;
 }
 
+// The same without a branch, for 16-bit elements of a row of at least eight, in two halves so that
+// the load can be far ahead of its use: the bytes are always loaded, from the row's last eight
+// elements where the chunk passes its end, from `any`, some readable 16 bytes, where it lies behind
+// it; settle_chunk shifts and zeroes them.
+__device__ __forceinline__ u32x4_t load_chunk_raw(const uint8_t* p, int valid,
+                                                  const uint8_t* any) {
+  const int miss = min(max(8 - valid, 0), 8);  // elements that do not exist
+  return *reinterpret_cast<const u32x4_any_t*>(miss == 8 ? any : p - 2 * miss);
+}
+
+__device__ __forceinline__ u32x4_t settle_chunk(u32x4_t r, int valid) {
+  const int miss = min(max(8 - valid, 0), 8);
+  uint32_t a = r[0], b = r[1], c = r[2], d = r[3];
+  if (miss & 1) {  // down by 16 bits, then by whole words; conditional moves
+    a = __builtin_amdgcn_alignbit(b, a, 16);
+    b = __builtin_amdgcn_alignbit(c, b, 16);
+    c = __builtin_amdgcn_alignbit(d, c, 16);
+    d >>= 16;
+  }
+  if (miss & 2) {
+    a = b;
+    b = c;
+    c = d;
+    d = 0;
+  }
+  if (miss & 4) {
+    a = c;
+    b = d;
+    c = d = 0;
+  }
+  if (miss == 8) a = b = c = d = 0;
+  return u32x4_t{a, b, c, d};
+}
+
 // ------------------------------------------------------------------------------------------------
 // Expert rows and M tiles from the device-side offsets, which the host never reads. Offsets are
 // clamped into [0, R] and to ascending order, so no value makes a kernel leave its buffers.

@@ -1,18 +1,22 @@
 // Ragged grouped products: out[r] = rows[r] W[e(r)], the two gradients, and the int8 forms, with
 // plain (unprepared) 16-bit weights in either order and any sizes.
 //
-// The tile kernel. A workgroup of four waves computes BN output columns x BM output rows, 128
-// bytes of the sum index per stage: each thread loads its 16-byte chunks of the next stage into
-// registers while the MFMAs run on the current one, and writes them to the other half of a
-// double-buffered LDS image. Chunks that pass the end of a row, of the columns or of an expert's
-// rows are zero in LDS, so every size is covered by the same loop and nothing that lies behind an
-// expert's rows (another expert's infinities, unwritten memory) enters a sum.
+// Two families of tiles. ProductBig (moe_product_big.h) brings its operands to LDS by direct loads
+// and takes what those can address; ProductTile below takes everything else: row pitches that are no
+// multiple of 16 bytes, sums and widths that are no whole chunks, gathered weight gradients. A
+// thread loads its 16-byte chunks of the stages ahead into registers while the MFMAs run, and
+// writes them to the other half of a double-buffered LDS image. In the stage that passes the end of
+// the sum, what lies behind it is zero in LDS, so nothing there (another expert's infinities,
+// unwritten memory) enters a sum; rows and columns behind the tile's edge repeat its last ones and
+// are not stored.
 #include "moe_product_big.h"
 
 namespace moe {
 namespace {
 
-template <int EL, int NK, int MK, int BN, int BM, int WN>
+// PF: stages in registers ahead of the one in LDS. TINY: an operand's rows are shorter than a chunk
+// (8 elements), everything is loaded element by element.
+template <int EL, int NK, int MK, int BN, int BM, int WN, int PF, bool TINY>
 struct ProductTile {
   static constexpr int WM = 4 / WN;            // waves along the rows
   static constexpr int NI = BN / WN / 16;      // n fragments per wave
@@ -40,7 +44,7 @@ struct ProductTile {
 
     const uint8_t* nb = p.n_base + (size_t)e * p.n_estride;
     const uint8_t* nsrc[NQ];
-    int nlim[NQ];  // contiguous: 1 if the row exists; strided: columns left from the chunk
+    int nlim[NQ];  // strided: columns left from the chunk
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
       const int id = q * 256 + tid;
@@ -48,14 +52,11 @@ struct ProductTile {
         const int kk = id / (BN / 8), c = id % (BN / 8);
         nsrc[q] = nb + (size_t)(k_lo + kk) * p.n_pitch + (size_t)(n0 + 8 * c) * EB;
         nlim[q] = p.N - (n0 + 8 * c);
-      } else if constexpr (NK == kOpPanel) {
-        const int n = n0 + (id >> 3), c = id & 7;
-        nsrc[q] = nb + (size_t)(n >> 4) * p.n_pitch + (n & 15) * 128 + 16 * c;
-        nlim[q] = n < p.N;
       } else {
-        const int n = n0 + (id >> 3), c = id & 7;
-        nsrc[q] = nb + (size_t)n * p.n_pitch + 16 * c;
-        nlim[q] = n < p.N;
+        const int n = min(n0 + (id >> 3), p.N - 1), c = id & 7;
+        nsrc[q] = NK == kOpPanel
+                      ? nb + (size_t)(n >> 4) * p.n_pitch + (n & 15) * 128 + 16 * c
+                      : nb + (size_t)n * p.n_pitch + 16 * c;
       }
     }
     const uint8_t* msrc[MQ];
@@ -68,53 +69,64 @@ struct ProductTile {
         msrc[q] = p.m_base + (size_t)(row0 + 8 * c) * EB;
         mlim[q] = p.M - (row0 + 8 * c);
       } else {
-        const int r = row0 + (id >> 3), c = id & 7;
-        const bool ok = r < row_end;
-        msrc[q] = p.m_base + (ok ? (size_t)source_row(p, r) * p.m_pitch : 0) + 16 * c;
-        mlim[q] = ok;
+        const int r = min(row0 + (id >> 3), row_end - 1), c = id & 7;
+        msrc[q] = p.m_base + (size_t)source_row(p, r) * p.m_pitch + 16 * c;
       }
     }
 
-    u32x4_t nreg[NQ], mreg[MQ];
-    auto fetch = [&](int j) {  // stage j into registers
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        const int id = q * 256 + tid;
-        if constexpr (NK == kOpKs) {
-          const int kk = id / (BN / 8);
-          const bool ok = j * BK + kk < klen;
-          nreg[q] = load_chunk<EB>(nsrc[q] + (size_t)j * BK * p.n_pitch, ok ? nlim[q] : 0);
-        } else if constexpr (NK == kOpPanel) {
-          nreg[q] = load_chunk<EB>(nsrc[q] + (size_t)j * 2048, nlim[q] ? 16 : 0);
-        } else {
-          nreg[q] = load_chunk<EB>(nsrc[q] + (size_t)j * 128,
-                                   nlim[q] ? klen - (j * BK + (id & 7) * (16 / EB)) : 0);
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < MQ; ++q) {
-        const int id = q * 256 + tid;
-        if constexpr (MK == kOpKs) {
-          const int kk = j * BK + id / (BM / 8);
-          const bool ok = kk < klen;
-          const size_t r = ok ? (size_t)source_row(p, k_lo + kk) : 0;
-          mreg[q] = load_chunk<EB>(msrc[q] + r * p.m_pitch, ok ? mlim[q] : 0);
-        } else if constexpr (EL == kPeI8) {  // code rows are padded to whole stages
-          mreg[q] = load_chunk<EB>(msrc[q] + (size_t)j * 128, mlim[q] ? 16 : 0);
-        } else {
-          mreg[q] = load_chunk<EB>(msrc[q] + (size_t)j * 128,
-                                   mlim[q] ? klen - (j * BK + (id & 7) * (16 / EB)) : 0);
-        }
-      }
+    struct Chunks {
+      u32x4_t n[NQ], m[MQ];
     };
-    auto put = [&](int b) {  // registers into LDS half b
-      uint8_t* s = lds + b * kStage;
+    // Elements of thread chunk q of stage j that exist, and (uniform) whether every chunk of the
+    // stage may be taken as it lies: not past the end of the sum, nor, strided, in a tile whose
+    // last columns are no whole chunk. (Code rows and panels are padded to whole stages.)
+    auto n_valid = [&](int j, int q) {
+      const int id = q * 256 + tid;
+      if constexpr (NK == kOpKs) return j * BK + id / (BN / 8) < klen ? nlim[q] : 0;
+      else return klen - (j * BK + (id & 7) * (16 / EB));
+    };
+    auto m_valid = [&](int j, int q) {
+      const int id = q * 256 + tid;
+      if constexpr (MK == kOpKs) return j * BK + id / (BM / 8) < klen ? mlim[q] : 0;
+      else return klen - (j * BK + (id & 7) * (16 / EB));
+    };
+    const bool n_even = !TINY && (NK != kOpKs || n0 + BN <= p.N);
+    const bool m_even = !TINY && (MK != kOpKs || row0 + BM <= p.M);
+    auto exact = [&](int j, bool even) {
+      return EL == kPeI8 || (even && (j + 1) * BK <= klen);
+    };
+    auto load = [&](bool whole, const uint8_t* at, int valid, const uint8_t* any) {
+      if (whole) return *reinterpret_cast<const u32x4_any_t*>(at);
+      if constexpr (TINY) return load_chunk<EB>(at, valid);
+      else return load_chunk_raw(at, valid, any);
+    };
+    auto fetch = [&](int j, Chunks& x) {  // stage j's loads into registers
+      const size_t step = NK == kOpKs ? BK * p.n_pitch : NK == kOpPanel ? 2048 : 128;
+      const bool ne = exact(j, n_even), me = exact(j, m_even);
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
-        *reinterpret_cast<u32x4_t*>(s + stage_byte<NK, BN>(q * 256 + tid)) = nreg[q];
+        x.n[q] = load(ne, nsrc[q] + (size_t)j * step, n_valid(j, q), nb);
+#pragma unroll
+      for (int q = 0; q < MQ; ++q) {
+        size_t at = (size_t)j * 128;
+        if constexpr (MK == kOpKs) {
+          const int kk = j * BK + (q * 256 + tid) / (BM / 8);
+          at = (size_t)source_row(p, k_lo + min(kk, klen - 1)) * p.m_pitch;
+        }
+        x.m[q] = load(me, msrc[q] + at, m_valid(j, q), p.m_base);
+      }
+    };
+    auto put = [&](int j, const Chunks& x) {  // stage j's registers into LDS half j % 2
+      uint8_t* s = lds + (j & 1) * kStage;
+      const bool ne = TINY || exact(j, n_even), me = TINY || exact(j, m_even);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+        *reinterpret_cast<u32x4_t*>(s + stage_byte<NK, BN>(q * 256 + tid)) =
+            ne ? x.n[q] : settle_chunk(x.n[q], n_valid(j, q));
 #pragma unroll
       for (int q = 0; q < MQ; ++q)
-        *reinterpret_cast<u32x4_t*>(s + BN * 128 + stage_byte<MK, BM>(q * 256 + tid)) = mreg[q];
+        *reinterpret_cast<u32x4_t*>(s + BN * 128 + stage_byte<MK, BM>(q * 256 + tid)) =
+            me ? x.m[q] : settle_chunk(x.m[q], m_valid(j, q));
     };
 
     Acc acc[NI][NJ];
@@ -127,29 +139,42 @@ struct ProductTile {
 
     const int nfrag = fragment_base<NK, BN>(wn * (BN / WN), lane);
     const int mfrag = fragment_base<MK, BM>(wm * (BM / WM), lane);
-    if (stages > 0) {
-      fetch(0);
-      put(0);
-    }
-    for (int j = 0; j < stages; ++j) {
+    // stage j from LDS half j % 2, `next` holding stage j + 1 and being refilled with j + 1 + PF
+    auto stage = [&](int j, Chunks& next, Chunks& far) {
       __syncthreads();
-      if (j + 1 < stages) fetch(j + 1);
+      // (no condition: behind a branch the compiler would wait for these loads before it uses the
+      // ones in front of them; past the end the last stage is loaded again and not used)
+      fetch(min(j + PF, stages - 1), PF == 1 ? next : far);
       const uint8_t* s = lds + (j & 1) * kStage;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         u32x4_t a[NI], b[NJ];
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-          a[i] = read_fragment<NK, BN>(s, nfrag, i, t);
+        for (int i = 0; i < NI; ++i) a[i] = read_fragment<NK, BN>(s, nfrag, i, t);
 #pragma unroll
-        for (int i = 0; i < NJ; ++i)
-          b[i] = read_fragment<MK, BM>(s + BN * 128, mfrag, i, t);
+        for (int i = 0; i < NJ; ++i) b[i] = read_fragment<MK, BM>(s + BN * 128, mfrag, i, t);
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
           for (int q = 0; q < NJ; ++q) acc[i][q] = product_mfma<EL>(a[i], b[q], acc[i][q]);
       }
-      if (j + 1 < stages) put((j + 1) & 1);
+      if (j + 1 < stages) put(j + 1, next);
+    };
+    Chunks x0, x1;
+    if (stages > 0) {
+      fetch(0, x0);
+      if (PF == 2) fetch(min(1, stages - 1), x1);
+      put(0, x0);
+    }
+    if constexpr (PF == 1) {
+      for (int j = 0; j < stages; ++j) stage(j, x0, x0);
+    } else {  // stage j + 1 waits in x1 for even j, in x0 for odd j
+      int j = 0;
+      for (; j + 1 < stages; j += 2) {
+        stage(j, x1, x0);
+        stage(j + 1, x0, x1);
+      }
+      if (j < stages) stage(j, x1, x0);
     }
 
     // acc[i][j][q]: column n0 + wn BN/WN + 16 i + 4 (lane / 16) + q,
@@ -207,16 +232,17 @@ __device__ __forceinline__ void product_tiles(const ProductArgs& p, uint8_t* lds
   }
 }
 
-template <int EL, int NK, int MK, int BN, int BM, int WN>
+template <int EL, int NK, int MK, int BN, int BM, int WN, int PF, bool TINY>
 __global__ __launch_bounds__(256, 2) void product_tile_kernel(ProductArgs p) {
-  using Tile = ProductTile<EL, NK, MK, BN, BM, WN>;
+  using Tile = ProductTile<EL, NK, MK, BN, BM, WN, PF, TINY>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[Tile::kLds];
   __shared__ int scratch[4];
   product_tiles<Tile, BN, BM, 4>(p, lds, scratch);
 }
 
-template <int EL, int NK, int MK, int BN, int BM, int WN, int WM, int NSN, int NSM>
-__global__ __launch_bounds__(64 * WN * WM, WN * WM / 4) void product_big_kernel(ProductArgs p) {
+// OCC: workgroups per CU
+template <int EL, int NK, int MK, int BN, int BM, int WN, int WM, int NSN, int NSM, int OCC>
+__global__ __launch_bounds__(64 * WN * WM, OCC * WN * WM / 4) void product_big_kernel(ProductArgs p) {
   using Tile = ProductBig<EL, NK, MK, BN, BM, WN, WM, NSN, NSM>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[Tile::kLds];
   const int nt_total = (p.N + BN - 1) / BN;
@@ -254,23 +280,43 @@ unsigned product_grid(long long tiles, long long slots) {
   return (unsigned)((g + 7) / 8 * 8);
 }
 
-template <int EL, int NK, int MK, int BN, int BM, int WN>
+template <int EL, int NK, int MK, int BN, int BM, int WN, int PF>
 hipError_t launch_tile(const ProductArgs& p, long long tiles, hipStream_t st) {
-  hipLaunchKernelGGL((product_tile_kernel<EL, NK, MK, BN, BM, WN>), dim3(product_grid(tiles, 512)),
-                     dim3(256), 0, st, p);
+  const dim3 g(product_grid(tiles, 512)), b(256);
+  const bool tiny = EL != kPeI8 && ((NK == kOpKs ? p.N : p.K) < 8 || (MK == kOpKs ? p.M : p.K) < 8);
+  if constexpr (BM <= 64 && EL != kPeI8) {
+    if (tiny) {
+      hipLaunchKernelGGL((product_tile_kernel<EL, NK, MK, BN, BM, WN, PF, true>), g, b, 0, st, p);
+      return hipGetLastError();
+    }
+  }
+  if (tiny) return hipErrorInvalidValue;  // (the callers send tiny rows to the 64-row tile)
+  hipLaunchKernelGGL((product_tile_kernel<EL, NK, MK, BN, BM, WN, PF, false>), g, b, 0, st, p);
   return hipGetLastError();
 }
 
-template <int EL, int NK, int MK, int BN, int BM, int WN, int WM, int NSN, int NSM>
+template <int EL, int NK, int MK, int BN, int BM, int WN, int WM, int NSN, int NSM, int OCC>
 hipError_t launch_big(const ProductArgs& p, long long tiles, hipStream_t st) {
-  hipLaunchKernelGGL((product_big_kernel<EL, NK, MK, BN, BM, WN, WM, NSN, NSM>),
-                     dim3(product_grid(tiles, 256)), dim3(64 * WN * WM), 0, st, p);
+  hipLaunchKernelGGL((product_big_kernel<EL, NK, MK, BN, BM, WN, WM, NSN, NSM, OCC>),
+                     dim3(product_grid(tiles, 256 * OCC)), dim3(64 * WN * WM), 0, st, p);
   return hipGetLastError();
 }
 
-// M tiles of bm rows that R rows over E experts can need
+// M tiles of bm rows that R rows over E experts can need, and (for the choice of a tile) that they
+// need when the last tile of an expert is half full
 long long row_tiles(const ProductArgs& p, int bm) {
   return (long long)(p.R / bm) + (p.E < p.R ? p.E : p.R);
+}
+long long likely_row_tiles(const ProductArgs& p, int bm) {
+  return (long long)(p.R / bm) + ((p.E < p.R ? p.E : p.R) + 1) / 2;
+}
+
+// Relative time of `tiles` tiles of which `slots` run at once, each round taking `unit`. Units, in
+// rounds of the 256 x 256 tile (8192 x 4096 x 4096 and the sizes around it, measured): 256 x 128
+// runs at 0.87 of its rate, 0.57; two 64 x 64 tiles per CU at about half of it, 0.25; of the
+// register-staged tiles 128 x 128 takes 2.7 rounds of 64 x 64.
+double tile_cost(long long tiles, int slots, double unit) {
+  return (double)((tiles + slots - 1) / slots) * unit;
 }
 
 // what the large tile's direct loads and stores need: rows at 16-byte steps, a sum (16-bit types)
@@ -285,35 +331,67 @@ bool big_rows_ok(const ProductArgs& p) {
   return !p.row_src || (unsigned long long)p.src_rows * p.m_pitch < (1ull << 32);
 }
 
+// The tile of a product over routed rows: the one whose rounds over the CUs are estimated cheapest
+// (a large tile has the higher rate, a small one fills the CUs and wastes less at an expert's
+// end), and 32 rows where an expert has at most 32 on average: reading the weights is all there
+// is, and the smallest tile has the most loads in flight for them.
 template <int EL, int NK>
 hipError_t launch_rows(ProductArgs& p, hipStream_t st) {
   const long long rpe = (p.R + p.E - 1) / p.E;
-  if (rpe > 64 && p.N >= 256 && big_rows_ok<NK>(p)) {
-    const int bm = rpe >= 384 ? 256 : 128, nt = (p.N + 255) / 256;
-    p.band_gm = band_groups_for(nt, bm, rpe);
-    if (bm == 256) return launch_big<EL, NK, kOpKc, 256, 256, 2, 2, 3, 2>(p, row_tiles(p, bm) * nt, st);
-    return launch_big<EL, NK, kOpKc, 256, 128, 2, 2, 3, 3>(p, row_tiles(p, bm) * nt, st);
+  const int n256 = (p.N + 255) / 256, n128 = (p.N + 127) / 128, n64 = (p.N + 63) / 64;
+  const double c64 = tile_cost(likely_row_tiles(p, 64) * n64, 512, 0.25);
+  const bool direct = big_rows_ok<NK>(p);
+  if (rpe <= 32) {
+    const long long tiles = row_tiles(p, 32) * n128;
+    p.band_gm = band_groups_for(n128, 32, rpe);
+    // (many tiles keep the memory busy with either; the register-staged one has less to set up)
+    if (direct && tiles < 1024)
+      return launch_big<EL, NK, kOpKc, 128, 32, 4, 1, 4, 4, 2>(p, tiles, st);
+    return launch_tile<EL, NK, kOpKc, 128, 32, 4, 2>(p, tiles, st);
   }
-  const int bm = rpe <= 32 ? 32 : (rpe <= 64 ? 64 : 128);
-  const int nt = (p.N + 127) / 128;
-  p.band_gm = band_groups_for(nt, bm, rpe);
-  const long long tiles = row_tiles(p, bm) * nt;
-  if (bm == 32) return launch_tile<EL, NK, kOpKc, 128, 32, 4>(p, tiles, st);
-  if (bm == 64) return launch_tile<EL, NK, kOpKc, 128, 64, 2>(p, tiles, st);
-  return launch_tile<EL, NK, kOpKc, 128, 128, 2>(p, tiles, st);
+  if (direct) {
+    const double c256 = tile_cost(likely_row_tiles(p, 256) * n256, 256, 1.0);
+    const double c128 = tile_cost(likely_row_tiles(p, 128) * n256, 256, 0.57);
+    if (c256 <= c128 && c256 <= c64) {
+      p.band_gm = band_groups_for(n256, 256, rpe);
+      return launch_big<EL, NK, kOpKc, 256, 256, 2, 2, 3, 2, 1>(p, row_tiles(p, 256) * n256, st);
+    }
+    if (c128 <= c64) {
+      p.band_gm = band_groups_for(n256, 128, rpe);
+      return launch_big<EL, NK, kOpKc, 256, 128, 2, 2, 3, 3, 1>(p, row_tiles(p, 128) * n256, st);
+    }
+    p.band_gm = band_groups_for(n64, 64, rpe);
+    return launch_big<EL, NK, kOpKc, 64, 64, 2, 2, 4, 4, 2>(p, row_tiles(p, 64) * n64, st);
+  }
+  if (p.K >= 8 && p.N >= 8 &&
+      tile_cost(likely_row_tiles(p, 128) * n128, 512, 2.7) <=
+          tile_cost(likely_row_tiles(p, 64) * n64, 512, 1.0)) {
+    p.band_gm = band_groups_for(n128, 128, rpe);
+    return launch_tile<EL, NK, kOpKc, 128, 128, 2, 1>(p, row_tiles(p, 128) * n128, st);
+  }
+  p.band_gm = band_groups_for(n64, 64, rpe);
+  return launch_tile<EL, NK, kOpKc, 64, 64, 2, 2>(p, row_tiles(p, 64) * n64, st);
 }
 
 template <int EL>
 hipError_t launch_wgrad(ProductArgs& p, hipStream_t st) {
-  if (p.m_pitch % 16 == 0 && p.n_pitch % 16 == 0 && p.M % 8 == 0 && p.N % 8 == 0 && !p.row_src &&
-      p.M >= 256 && p.N >= 256) {
-    const int nt = (p.N + 255) / 256, mt = (p.M + 255) / 256;
-    p.band_gm = band_groups_for(nt, 256, p.M);
-    return launch_big<EL, kOpKs, kOpKs, 256, 256, 2, 2, 3, 2>(p, (long long)mt * nt * p.E, st);
+  auto tiles = [&](int b) { return (long long)((p.M + b - 1) / b) * ((p.N + b - 1) / b) * p.E; };
+  auto band = [&](int b) { return band_groups_for((p.N + b - 1) / b, b, p.M); };
+  const long long t256 = tiles(256), t128 = tiles(128), t64 = tiles(64);
+  if (p.m_pitch % 16 == 0 && p.n_pitch % 16 == 0 && p.M % 8 == 0 && p.N % 8 == 0 && !p.row_src) {
+    if (tile_cost(t256, 256, 1.0) <= tile_cost(t64, 512, 0.25)) {
+      p.band_gm = band(256);
+      return launch_big<EL, kOpKs, kOpKs, 256, 256, 2, 2, 3, 2, 1>(p, t256, st);
+    }
+    p.band_gm = band(64);
+    return launch_big<EL, kOpKs, kOpKs, 64, 64, 2, 2, 4, 4, 2>(p, t64, st);
   }
-  const int nt = (p.N + 127) / 128, mt = (p.M + 127) / 128;
-  p.band_gm = band_groups_for(nt, 128, p.M);
-  return launch_tile<EL, kOpKs, kOpKs, 128, 128, 2>(p, (long long)mt * nt * p.E, st);
+  if (p.M >= 8 && p.N >= 8 && tile_cost(t128, 512, 2.7) <= tile_cost(t64, 512, 1.0)) {
+    p.band_gm = band(128);
+    return launch_tile<EL, kOpKs, kOpKs, 128, 128, 2, 1>(p, t128, st);
+  }
+  p.band_gm = band(64);
+  return launch_tile<EL, kOpKs, kOpKs, 64, 64, 2, 2>(p, t64, st);
 }
 
 }  // namespace
