@@ -415,6 +415,8 @@ typedef struct {
  *   int32 and src(r) = row_src[r] / row_div: with perm and k of moe_permute, token perm[r] / k, so
  *   the routed rows need not be written out. (moe_grouped_gemm_wgrad: the index is of `rows`; dy
  *   is in routed order.)
+ * ws of moe_grouped_gemm_wgrad: moe_grouped_gemm_wgrad_workspace_bytes() bytes of scratch (a small
+ *   gradient over many rows is summed in parts, which are added in a fixed order).
  * Rows outside every expert's range (behind offsets[E], dropped assignments) are neither read nor
  * written; an expert without rows has a zero weight gradient.
  * MOE_EINVAL: a null or misaligned pointer, a pitch below the row's width, an unknown or
@@ -428,10 +430,12 @@ moe_status moe_grouped_gemm_dgrad(const moe_gemm_shape* s, moe_elt dt, const voi
                                   int64_t ld_dy, const int32_t* row_src, int32_t row_div,
                                   int32_t src_rows, const void* w, const int32_t* offsets,
                                   void* dx, int64_t ld_dx, moe_elt out_dt, void* stream);
+size_t moe_grouped_gemm_wgrad_workspace_bytes(const moe_gemm_shape* s);
 moe_status moe_grouped_gemm_wgrad(const moe_gemm_shape* s, moe_elt dt, const void* rows,
                                   int64_t ld_rows, const int32_t* row_src, int32_t row_div,
                                   int32_t src_rows, const void* dy, int64_t ld_dy,
-                                  const int32_t* offsets, void* dw, moe_elt dw_dt, void* stream);
+                                  const int32_t* offsets, void* dw, moe_elt dw_dt, void* ws,
+                                  void* stream);
 
 /* ---------------------------------------------------------------------------------------------
  * Int8 products with a scale per token and per weight column.

@@ -19,7 +19,8 @@ from ._lib import (BWD_STAGES, MOE_BF16, MOE_BWD_PROFILE_EVENTS, MOE_MXFP8,
                    MOE_PERMUTE_STATIC_SCRATCH_BYTES, MOE_PROFILE_EVENTS, STAGES, MoeError,
                    MoeForwardViews, MoeShape, check, load)
 from .products import (make_gemm_shape, moe_gemm_int8, moe_grouped_gemm, moe_grouped_gemm_dgrad,
-                       moe_grouped_gemm_int8, moe_grouped_gemm_wgrad, moe_int8_pack_weights,
+                       moe_grouped_gemm_int8, moe_grouped_gemm_wgrad,
+                       moe_grouped_gemm_wgrad_workspace_bytes, moe_int8_pack_weights,
                        moe_int8_pitch, moe_int8_prepare_weights, moe_int8_weight_bytes,
                        moe_quantize_int8)
 from .norms import (moe_norm_backward_workspace_bytes, moe_post_norm, moe_post_norm_backward,
@@ -36,7 +37,8 @@ __all__ = [
     "moe_saved_bytes", "moe_prepared_bwd_weight_bytes", "moe_prepare_bwd_weights",
     "moe_backward_workspace_bytes", "moe_backward", "moe_backward_layer",
     "moe_backward_profiled",
-    "make_gemm_shape", "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad",
+    "make_gemm_shape", "moe_grouped_gemm", "moe_grouped_gemm_dgrad",
+    "moe_grouped_gemm_wgrad_workspace_bytes", "moe_grouped_gemm_wgrad",
     "moe_int8_pitch", "moe_quantize_int8", "moe_int8_weight_bytes", "moe_int8_pack_weights",
     "moe_int8_prepare_weights", "moe_gemm_int8", "moe_grouped_gemm_int8", "moe_pre_norm",
     "moe_pre_norm_int8", "moe_post_norm", "moe_norm_backward_workspace_bytes",

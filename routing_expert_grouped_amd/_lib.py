@@ -30,7 +30,8 @@ EXPORTS = [
     "moe_saved_bytes", "moe_prepared_bwd_weight_bytes", "moe_prepare_bwd_weights",
     "moe_backward_workspace_bytes", "moe_backward", "moe_backward_layer",
     "moe_backward_profiled",
-    "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad",
+    "moe_grouped_gemm", "moe_grouped_gemm_dgrad",
+    "moe_grouped_gemm_wgrad_workspace_bytes", "moe_grouped_gemm_wgrad",
     "moe_int8_pitch", "moe_quantize_int8", "moe_int8_weight_bytes", "moe_int8_pack_weights",
     "moe_int8_prepare_weights", "moe_gemm_int8", "moe_grouped_gemm_int8",
     "moe_pre_norm", "moe_post_norm", "moe_norm_backward_workspace_bytes",
@@ -115,7 +116,8 @@ def load() -> ctypes.CDLL:
         "moe_backward_profiled": (I, [S, I, P, P, P, P, P, P, P, P, I, P, P, P]),
         "moe_grouped_gemm": (I, [Q, I, P, L, P, N, N, P, P, P, L, I, P]),
         "moe_grouped_gemm_dgrad": (I, [Q, I, P, L, P, N, N, P, P, P, L, I, P]),
-        "moe_grouped_gemm_wgrad": (I, [Q, I, P, L, P, N, N, P, L, P, P, I, P]),
+        "moe_grouped_gemm_wgrad_workspace_bytes": (Z, [Q]),
+        "moe_grouped_gemm_wgrad": (I, [Q, I, P, L, P, N, N, P, L, P, P, I, P, P]),
         "moe_int8_pitch": (Z, [N]),
         "moe_quantize_int8": (I, [N, N, I, P, L, I, P, P, P]),
         "moe_int8_weight_bytes": (Z, [Q]),

@@ -168,17 +168,25 @@ moe_status moe_grouped_gemm_dgrad(const moe_gemm_shape* s, moe_elt dt, const voi
                          out_dt, stream);
 }
 
+size_t moe_grouped_gemm_wgrad_workspace_bytes(const moe_gemm_shape* s) {
+  if (check_gemm_shape(s) != MOE_OK) return 0;
+  const int split = wgrad_split(s->K, s->N, s->E, s->R);
+  const size_t parts = split > 1 ? (size_t)split * s->E * s->K * s->N * sizeof(float) : 0;
+  return align_up(parts + 1);
+}
+
 moe_status moe_grouped_gemm_wgrad(const moe_gemm_shape* s, moe_elt dt, const void* rows,
                                   int64_t ld_rows, const int32_t* row_src, int32_t row_div,
                                   int32_t src_rows, const void* dy, int64_t ld_dy,
-                                  const int32_t* offsets, void* dw, moe_elt dw_dt, void* stream) {
+                                  const int32_t* offsets, void* dw, moe_elt dw_dt, void* ws,
+                                  void* stream) {
   const moe_status st = check_gemm_shape(s);
   if (st != MOE_OK) return st;
   if (!elt_16bit(dt) || (dw_dt != dt && dw_dt != MOE_ELT_F32)) return MOE_EINVAL;
   if (ld_rows < s->K || ld_dy < s->N) return MOE_EINVAL;
   const moe_status g = check_gather(row_src, row_div, src_rows, s->R);
   if (g != MOE_OK) return g;
-  if (!aligned_ptr(dw) || !aligned_ptr(offsets) || !buffer_ok(rows, s->R) ||
+  if (!aligned_ptr(dw) || !aligned_ptr(offsets) || !aligned_ptr(ws) || !buffer_ok(rows, s->R) ||
       !buffer_ok(dy, s->R))
     return MOE_EINVAL;
   ProductArgs p{};
@@ -194,7 +202,7 @@ moe_status moe_grouped_gemm_wgrad(const moe_gemm_shape* s, moe_elt dt, const voi
   p.M = s->K;
   output_args(p, dw, (size_t)s->N, dw_dt);
   return hip_status(launch_grouped_wgrad(p, dt == MOE_ELT_FP16 ? kPeFp16 : kPeBf16,
-                                         as_stream(stream)));
+                                         reinterpret_cast<float*>(ws), as_stream(stream)));
 }
 
 size_t moe_int8_pitch(int32_t K) { return K < 1 ? 0 : int8_pitch(K); }

@@ -47,6 +47,7 @@ struct ProductArgs {
   int K;                   // sum length (weight gradients: unused, the expert's rows)
   int N;                   // output columns
   int M;                   // weight gradients: output rows per expert
+  int split;               // weight gradients: parts the rows of an expert are split into
   void* out;
   size_t out_ld;           // elements between output rows
   int out_kind;            // ProductOut
@@ -248,6 +249,17 @@ __device__ __forceinline__ void expert_rows(const ProductArgs& p, int e, int& lo
   hi = min(max(p.offsets[e + 1], lo), p.R);
 }
 
+// Rows of group g of a weight gradient: part g / E of the rows of expert g % E, parts of whole
+// stages (64 rows).
+__device__ __forceinline__ void wgrad_rows(const ProductArgs& p, int g, int& lo, int& hi) {
+  expert_rows(p, g % p.E, lo, hi);
+  if (p.split > 1) {
+    const int part = ((hi - lo + p.split - 1) / p.split + 63) / 64 * 64;
+    lo = min(lo + (g / p.E) * part, hi);
+    hi = min(lo + part, hi);
+  }
+}
+
 // The M tile table: first tile of each expert, by one scan per workgroup (the first 256 threads,
 // four experts each; scratch: one int per wave). Cheaper than a launch of its own for a small call
 // and invisible in a large one.
@@ -380,7 +392,9 @@ namespace moe {
 
 // Host launchers (moe_product_kernels.hip); each returns hipGetLastError() after enqueueing.
 hipError_t launch_grouped_gemm(ProductArgs p, int el, bool trans_w, hipStream_t st);
-hipError_t launch_grouped_wgrad(ProductArgs p, int el, hipStream_t st);
+// ws: wgrad_split(...) > 1 parts of [E][M][N] float each
+int wgrad_split(int M, int N, int E, int R);
+hipError_t launch_grouped_wgrad(ProductArgs p, int el, float* ws, hipStream_t st);
 hipError_t launch_int8_gemm(ProductArgs p, hipStream_t st);
 // the few-row form (moe_int8_few_kernels.hip), `rows` the rows per expert on average
 hipError_t launch_int8_few(ProductArgs p, int rows, hipStream_t st);

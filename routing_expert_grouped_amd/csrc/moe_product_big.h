@@ -195,7 +195,7 @@ struct ProductBig {
                                                     Source& s) {
     const int tid = threadIdx.x;
     int k_lo = 0, k_hi = p.K;
-    if constexpr (kWgrad) expert_rows(p, at.e, k_lo, k_hi);
+    if constexpr (kWgrad) wgrad_rows(p, at.e, k_lo, k_hi);
     const int klen = __builtin_amdgcn_readfirstlane(k_hi - k_lo);
     s.whole = klen / BK;
     s.left = klen - s.whole * BK;

@@ -38,7 +38,7 @@ struct ProductTile {
     const int wn = wave / WM, wm = wave % WM;
     // the sum index: K columns, or the expert's rows
     int k_lo = 0, k_hi = p.K;
-    if constexpr (kWgrad) expert_rows(p, e, k_lo, k_hi);
+    if constexpr (kWgrad) wgrad_rows(p, e, k_lo, k_hi);
     const int klen = k_hi - k_lo;
     const int stages = (klen + BK - 1) / BK;
 
@@ -216,7 +216,7 @@ __device__ __forceinline__ void product_tiles(const ProductArgs& p, uint8_t* lds
   if constexpr (Tile::kWgrad) {
     const int mt = (p.M + BM - 1) / BM;
     for (int jx = blockIdx.x >> 3;
-         big_tile_coords(mt * p.E, nt_total, p.band_gm, xcd, jx, ti, nt); jx += gridDim.x >> 3) {
+         big_tile_coords(mt * p.E * p.split, nt_total, p.band_gm, xcd, jx, ti, nt); jx += gridDim.x >> 3) {
       Tile::run(p, ti / mt, (ti % mt) * BM, 0, nt * BN, lds);
       __syncthreads();
     }
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(64 * WN * WM, OCC * WN * WM / 4) void product_big_k
     const int mt = (p.M + BM - 1) / BM;
     Tile::run(p, lds, [&](TileAt& at) {
       int ti, nt;
-      if (!big_tile_coords(mt * p.E, nt_total, p.band_gm, xcd, jx, ti, nt)) return false;
+      if (!big_tile_coords(mt * p.E * p.split, nt_total, p.band_gm, xcd, jx, ti, nt)) return false;
       jx += per;
       at.e = __builtin_amdgcn_readfirstlane(ti / mt);
       at.row0 = __builtin_amdgcn_readfirstlane((ti % mt) * BM);
@@ -308,6 +308,7 @@ long long row_tiles(const ProductArgs& p, int bm) {
   return (long long)(p.R / bm) + (p.E < p.R ? p.E : p.R);
 }
 long long likely_row_tiles(const ProductArgs& p, int bm) {
+  if (p.E == 1) return (p.R + bm - 1) / bm;
   return (long long)(p.R / bm) + ((p.E < p.R ? p.E : p.R) + 1) / 2;
 }
 
@@ -344,9 +345,7 @@ hipError_t launch_rows(ProductArgs& p, hipStream_t st) {
   if (rpe <= 32) {
     const long long tiles = row_tiles(p, 32) * n128;
     p.band_gm = band_groups_for(n128, 32, rpe);
-    // (many tiles keep the memory busy with either; the register-staged one has less to set up)
-    if (direct && tiles < 1024)
-      return launch_big<EL, NK, kOpKc, 128, 32, 4, 1, 4, 4, 2>(p, tiles, st);
+    if (direct) return launch_big<EL, NK, kOpKc, 128, 32, 4, 1, 4, 4, 2>(p, tiles, st);
     return launch_tile<EL, NK, kOpKc, 128, 32, 4, 2>(p, tiles, st);
   }
   if (direct) {
@@ -373,12 +372,60 @@ hipError_t launch_rows(ProductArgs& p, hipStream_t st) {
   return launch_tile<EL, NK, kOpKc, 64, 64, 2, 2>(p, row_tiles(p, 64) * n64, st);
 }
 
+// dw = the split parts added in order; four elements per thread
+__global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict__ part, int split,
+                                                         size_t count, void* __restrict__ out,
+                                                         int out_kind) {
+  const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= count) return;
+  f32x4v_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+  const bool whole = count % 4 == 0;  // (then every part starts at a 16-byte step)
+  for (int k = 0; k < split; ++k) {
+    const float* q = part + (size_t)k * count + i;
+    if (whole) {
+      s += *reinterpret_cast<const f32x4v_t*>(q);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < count) s[j] += q[j];
+    }
+  }
+  ProductArgs p{};  // (store_run's row: the rest of the array)
+  p.out = out;
+  p.out_kind = out_kind;
+  p.out_vec = whole;
+  p.N = count - i < 4 ? (int)(count - i) : 4;
+  store_run(p, i, 0, s);
+}
+
+long long wgrad_tiles(int M, int N, int E, int b) {
+  return (long long)((M + b - 1) / b) * ((N + b - 1) / b) * E;
+}
+
 template <int EL>
-hipError_t launch_wgrad(ProductArgs& p, hipStream_t st) {
-  auto tiles = [&](int b) { return (long long)((p.M + b - 1) / b) * ((p.N + b - 1) / b) * p.E; };
+hipError_t launch_wgrad(ProductArgs& p, float* ws, hipStream_t st) {
+  auto tiles = [&](int b) { return wgrad_tiles(p.M, p.N, p.E, b); };
   auto band = [&](int b) { return band_groups_for((p.N + b - 1) / b, b, p.M); };
   const long long t256 = tiles(256), t128 = tiles(128), t64 = tiles(64);
-  if (p.m_pitch % 16 == 0 && p.n_pitch % 16 == 0 && p.M % 8 == 0 && p.N % 8 == 0 && !p.row_src) {
+  const bool direct = p.m_pitch % 16 == 0 && p.n_pitch % 16 == 0 && p.M % 8 == 0 && p.N % 8 == 0 &&
+                      !p.row_src;
+  const int split = wgrad_split(p.M, p.N, p.E, p.R);
+  if (split > 1) {  // into parts [split][E][M][N], then their sum
+    ProductArgs q = p;
+    q.split = split;
+    q.out = ws;
+    q.out_kind = kOutF32;
+    q.band_gm = band(64);
+    const hipError_t e =
+        direct ? launch_big<EL, kOpKs, kOpKs, 64, 64, 2, 2, 4, 4, 2>(q, t64 * split, st)
+               : launch_tile<EL, kOpKs, kOpKs, 64, 64, 2, 2>(q, t64 * split, st);
+    if (e != hipSuccess) return e;
+    const size_t count = (size_t)p.E * p.M * p.N;
+    hipLaunchKernelGGL(wgrad_join_kernel, dim3((unsigned)((count + 1023) / 1024)), dim3(256), 0,
+                       st, ws, split, count, p.out, p.out_kind);
+    return hipGetLastError();
+  }
+  if (direct) {
     if (tile_cost(t256, 256, 1.0) <= tile_cost(t64, 512, 0.25)) {
       p.band_gm = band(256);
       return launch_big<EL, kOpKs, kOpKs, 256, 256, 2, 2, 3, 2, 1>(p, t256, st);
@@ -402,8 +449,20 @@ hipError_t launch_grouped_gemm(ProductArgs p, int el, bool trans_w, hipStream_t 
   return trans_w ? launch_rows<kPeFp16, kOpKc>(p, st) : launch_rows<kPeFp16, kOpKs>(p, st);
 }
 
-hipError_t launch_grouped_wgrad(ProductArgs p, int el, hipStream_t st) {
-  return el == kPeBf16 ? launch_wgrad<kPeBf16>(p, st) : launch_wgrad<kPeFp16>(p, st);
+// Parts the rows of each expert are split into: where the 64 x 64 tiles of a small gradient do not
+// fill the 512 places, as many as do, of at least 256 rows on average (what a part costs in
+// writing and adding), at most 32.
+int wgrad_split(int M, int N, int E, int R) {
+  const long long t64 = wgrad_tiles(M, N, E, 64);
+  long long s = 512 / t64;
+  const long long rows = R / (256ll * E);
+  s = s < rows ? s : rows;
+  return (int)(s < 1 ? 1 : s > 32 ? 32 : s);
+}
+
+hipError_t launch_grouped_wgrad(ProductArgs p, int el, float* ws, hipStream_t st) {
+  p.split = 1;
+  return el == kPeBf16 ? launch_wgrad<kPeBf16>(p, ws, st) : launch_wgrad<kPeFp16>(p, ws, st);
 }
 
 hipError_t launch_int8_gemm(ProductArgs p, hipStream_t st) {

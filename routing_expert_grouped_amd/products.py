@@ -18,7 +18,7 @@ from ._launch import ELT, Launch, elt16
 from ._lib import MoeError, MoeGemmShape, check, load
 
 __all__ = ["make_gemm_shape", "moe_grouped_gemm", "moe_grouped_gemm_dgrad",
-           "moe_grouped_gemm_wgrad", "moe_int8_pitch", "moe_quantize_int8",
+           "moe_grouped_gemm_wgrad_workspace_bytes", "moe_grouped_gemm_wgrad", "moe_int8_pitch", "moe_quantize_int8",
            "moe_int8_weight_bytes", "moe_int8_pack_weights", "moe_int8_prepare_weights",
            "moe_gemm_int8", "moe_grouped_gemm_int8"]
 
@@ -82,14 +82,22 @@ def moe_grouped_gemm_dgrad(shape, dy, w, offsets, perm=None, k: int = 1, out=Non
                          out_dtype, stream, shape.N, shape.K)
 
 
+def moe_grouped_gemm_wgrad_workspace_bytes(shape) -> int:
+    return load().moe_grouped_gemm_wgrad_workspace_bytes(byref(shape))
+
+
 def moe_grouped_gemm_wgrad(shape, rows, dy, offsets, perm=None, k: int = 1, dw=None,
-                           dw_dtype=torch.float32, stream=None):
+                           dw_dtype=torch.float32, ws=None, stream=None):
     """dw[e] = sum over the expert's rows of rows[src(r)]^T dy[r], [E][K][N] in float32 or the
     operands' type; an expert without rows gets zeros. Returns dw."""
     dt = elt16(rows, "rows")
     R, K, N, E = shape.R, shape.K, shape.N, shape.E
+    nws = moe_grouped_gemm_wgrad_workspace_bytes(shape)
+    if nws == 0:
+        raise MoeError("moe_grouped_gemm_wgrad_workspace_bytes", 1, "shape rejected")
     L = Launch(rows.device, stream)
     with L:
+        ws = L.empty(nws, dtype=torch.uint8) if ws is None else ws
         if dw is None:
             dw = L.empty(E, K, N, dtype=_out_dtype(dw_dtype, (rows.dtype, torch.float32)))
         else:
@@ -100,7 +108,8 @@ def moe_grouped_gemm_wgrad(shape, rows, dy, offsets, perm=None, k: int = 1, dw=N
         check("moe_grouped_gemm_wgrad", load().moe_grouped_gemm_wgrad(
             byref(shape), dt, rp, ld, src, div, n, dp, dld,
             L.dense(offsets, "offsets", torch.int32, E + 1),
-            L.dense(dw, "dw", dw.dtype, E, K, N), ELT[dw.dtype], L.handle))
+            L.dense(dw, "dw", dw.dtype, E, K, N), ELT[dw.dtype], L.buffer(ws, "ws", nws),
+            L.handle))
     return dw
 
 

@@ -92,6 +92,52 @@ def test_grouped_products_larger(shape):
     _close(dw, ref, P.product_bound(ref, mag, R, F32), "wgrad")
 
 
+@pytest.mark.parametrize("case", [([5000], 64, 64), ([3000, 0, 2100], 72, 40), ([9000], 65, 33),
+                                  ([1100, 1500], 1, 3), ([4000, 70], 200, 128)], ids=str)
+def test_weight_gradient_in_parts(case):
+    """Small gradients over many rows are summed in parts, added in a fixed order: within the bound,
+    the same twice, and with a caller's workspace."""
+    G = require_gpu()
+    counts, K, N = case
+    E, R = len(counts), sum(counts)
+    g = torch.Generator().manual_seed(K)
+    x, dy, off = _rand(g, R, K), _rand(g, R, N), _offsets(counts)
+    sh = G.make_gemm_shape(R, K, N, E)
+    nws = G.moe_grouped_gemm_wgrad_workspace_bytes(sh)
+    assert nws > 2 * E * K * N * 4
+    for odt in (F32, BF):
+        dw = G.moe_grouped_gemm_wgrad(sh, x.cuda(), dy.cuda(), _dev_i32(off),
+                                      dw=poisoned((E, K, N), odt))
+        ref, mag = P.wgrad(x, P.f8(dy), off)
+        _close(dw, ref, P.product_bound(ref, mag, max(counts), odt), case)
+        again = G.moe_grouped_gemm_wgrad(sh, x.cuda(), dy.cuda(), _dev_i32(off),
+                                         dw=poisoned((E, K, N), odt),
+                                         ws=poisoned((nws,), torch.uint8))
+        assert torch.equal(dw, again)
+    with pytest.raises(ValueError, match="ws"):
+        G.moe_grouped_gemm_wgrad(sh, x.cuda(), dy.cuda(), _dev_i32(off),
+                                 ws=torch.empty(nws - 1, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("case", [(1000, 4, 8, 256, 512), (40, 2, 2, 136, 264), (2000, 2, 3, 512, 72)],
+                         ids=str)
+def test_gather_through_perm(case):
+    """Tokens gathered through perm by the direct-load tiles, every row tile height."""
+    G = require_gpu()
+    T, k, E, K, N = case
+    R = T * k
+    g = torch.Generator().manual_seed(T)
+    assign = torch.randint(0, E, (R,), generator=g)
+    perm = torch.argsort(assign, stable=True).to(torch.int32)
+    off = _offsets(torch.bincount(assign, minlength=E).tolist())
+    x, w = _rand(g, T, K), _rand(g, E, K, N, scale=K ** -0.5)
+    sh = G.make_gemm_shape(R, K, N, E)
+    out = G.moe_grouped_gemm(sh, x.cuda(), w.cuda(), _dev_i32(off), perm=perm.cuda(), k=k,
+                             out=poisoned((R, N), BF))
+    ref, mag = P.grouped(x, w, off, (perm // k).long())
+    _close(out, ref, P.product_bound(ref, mag, K, BF), case)
+
+
 @pytest.mark.parametrize("dims", [(72, 136), (71, 33), (512, 256)], ids=str)
 def test_gather_strides_and_foreign_rows(dims):
     """Rows gathered through perm, rows and outputs that are column slices of wider tensors, and

@@ -60,11 +60,16 @@ def test_wgrad_refusals(lib):
     L = lib.load()
 
     def call(shape=None, dt=BF, rows=FAKE, ld=100, src=None, div=1, nsrc=64, dy=FAKE, ldy=60,
-             off=FAKE, dw=FAKE, wdt=F32):
+             off=FAKE, dw=FAKE, wdt=F32, ws=FAKE):
         return L.moe_grouped_gemm_wgrad(shape or _s(lib), dt, rows, ld, src, div, nsrc, dy, ldy,
-                                        off, dw, wdt, None)
+                                        off, dw, wdt, ws, None)
 
-    for kw in [dict(rows=None), dict(dy=None), dict(dw=None), dict(off=None), dict(dw=FAKE + 4),
+    # many rows into a small gradient: room for the parts; else next to none
+    assert L.moe_grouped_gemm_wgrad_workspace_bytes(_s(lib, R=8192, K=64, N=64, E=1)) >= \
+        2 * 64 * 64 * 4
+    assert 0 < L.moe_grouped_gemm_wgrad_workspace_bytes(_s(lib, R=100, K=64, N=64)) <= 256
+    assert L.moe_grouped_gemm_wgrad_workspace_bytes(_s(lib, R=-1)) == 0
+    for kw in [dict(ws=None), dict(ws=FAKE + 8), dict(rows=None), dict(dy=None), dict(dw=None), dict(off=None), dict(dw=FAKE + 4),
                dict(ld=99), dict(ldy=59), dict(wdt=HF), dict(dt=F32), dict(nsrc=10),
                dict(src=FAKE, div=-1)]:
         assert call(**kw) == lib.MOE_EINVAL, kw
