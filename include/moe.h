@@ -390,7 +390,7 @@ moe_status moe_backward_profiled(const moe_shape* s, moe_dtype dt, const uint16_
  * NULL. Offsets live on the device and are not read by the host; the kernels clamp them to
  * ascending values in [0, R], and source rows to [0, src_rows).
  * Beyond the sizes stated at a call: MOE_EUNSUPPORTED for R > 2^30, K or N > 2^20, E > 1024, or
- * more than 2^30 tiles of 32 rows x 128 columns.
+ * more than 2^30 tiles of 32 rows x 128 columns of an output or of 64 x 64 of the weights.
  * ------------------------------------------------------------------------------------------- */
 typedef enum { MOE_ELT_BF16 = 0, MOE_ELT_FP16 = 1, MOE_ELT_F32 = 2 } moe_elt;
 

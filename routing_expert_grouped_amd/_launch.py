@@ -15,19 +15,21 @@ ELT = {torch.bfloat16: MOE_ELT_BF16, torch.float16: MOE_ELT_FP16, torch.float32:
 
 class Launch:
     """Context of one call: `handle` is the hipStream_t; inside it, allocations belong to that
-    stream and the current device is the tensors' device."""
+    stream and the current device is the tensors' device. (A call on the current device and stream,
+    the usual one, enters nothing: the checks are a good part of a small call's time.)"""
 
-    __slots__ = ("device", "handle", "_guards")
+    __slots__ = ("device", "index", "handle", "_guards")
 
     def __init__(self, device: torch.device, stream=None):
         if device.type != "cuda":
             raise ValueError(f"need CUDA tensors, got {device}")
         self.device = device
+        self.index = device.index
         self._guards = ()
-        if device.index != torch.cuda.current_device():
+        if self.index != torch.cuda.current_device():
             self._guards = (torch.cuda.device(device),)
         if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
+            self.handle = torch._C._cuda_getCurrentRawStream(self.index)
         else:
             if not isinstance(stream, torch.cuda.Stream):
                 stream = torch.cuda.ExternalStream(int(stream), device=device)
@@ -54,8 +56,9 @@ class Launch:
         None."""
         if t is None:
             return None
-        self._check(t, name, dtype)
-        if tuple(t.shape) != shape:
+        if t.dtype is not dtype or t.get_device() != self.index:
+            self._refuse(t, name, dtype)
+        if t.shape != shape:
             raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
         if not t.is_contiguous():
             raise ValueError(f"{name}: need a contiguous tensor")
@@ -64,21 +67,25 @@ class Launch:
     def rows(self, t, name, dtype, cols, nrows=None):
         """(pointer, row pitch, rows) of a 2-D tensor whose rows are contiguous; the rows may be
         further apart than they are long (a column slice of a wider tensor)."""
-        self._check(t, name, dtype)
-        if t.dim() != 2 or t.shape[1] != cols or (nrows is not None and t.shape[0] != nrows):
+        if t.dtype is not dtype or t.get_device() != self.index:
+            self._refuse(t, name, dtype)
+        shape = t.shape
+        if len(shape) != 2 or shape[1] != cols or (nrows is not None and shape[0] != nrows):
             want = ("rows" if nrows is None else nrows, cols)
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {want}")
-        n, ld = t.shape[0], t.stride(0)
+            raise ValueError(f"{name}: shape {tuple(shape)}, expected {want}")
+        n = shape[0]
+        ld, step = t.stride()
         if n <= 1:
             ld = max(ld, cols)
-        if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        if (cols > 1 and step != 1) or ld < cols:
             raise ValueError(f"{name}: strides {t.stride()}: need contiguous rows that do not "
                              "overlap")
         return t.data_ptr(), ld, n
 
     def buffer(self, t, name, nbytes):
         """Pointer of a contiguous buffer of at least nbytes bytes."""
-        self._check(t, name, t.dtype)
+        if t.get_device() != self.index:
+            self._refuse(t, name, t.dtype)
         if not t.is_contiguous():
             raise ValueError(f"{name}: need a contiguous tensor")
         have = t.numel() * t.element_size()
@@ -86,7 +93,7 @@ class Launch:
             raise ValueError(f"{name}: {have} bytes, the shape needs {nbytes}")
         return t.data_ptr()
 
-    def _check(self, t, name, dtype):
+    def _refuse(self, t, name, dtype):
         if t.device != self.device:
             raise ValueError(f"{name}: on {t.device}, expected {self.device}")
         if t.dtype != dtype:

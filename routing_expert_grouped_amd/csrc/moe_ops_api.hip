@@ -35,6 +35,9 @@ moe_status check_gemm_shape(const moe_gemm_shape* s) {
   const long long mt = (long long)s->R / 32 + s->E + 1;
   const long long w = s->K > s->N ? s->K : s->N;
   if (mt * (w / 128 + 1) > (1ll << 30)) return MOE_EUNSUPPORTED;
+  // and those of a weight gradient, 64 x 64
+  if ((long long)s->E * ((s->K + 63) / 64) * ((s->N + 63) / 64) > (1ll << 30))
+    return MOE_EUNSUPPORTED;
   return MOE_OK;
 }
 

@@ -187,7 +187,7 @@ def test_binding_checks_without_gpu():
 
     cpu = torch.device("cpu")
     L = Launch.__new__(Launch)
-    L.device, L.handle, L._guards = cpu, 0, ()
+    L.device, L.index, L.handle, L._guards = cpu, -1, 0, ()
     wide = torch.zeros(6, 20, dtype=torch.float16)
     assert L.rows(wide[:, 4:12], "x", torch.float16, 8)[1:] == (20, 6)
     assert L.rows(wide[:1, 4:12], "x", torch.float16, 8)[1:] == (20, 1)
