@@ -392,6 +392,7 @@ moe_status moe_backward_profiled(const moe_shape* s, moe_dtype dt, const uint16_
  * Beyond the sizes stated at a call: MOE_EUNSUPPORTED for R > 2^30, K or N > 2^20, E > 1024, or
  * more than 2^30 tiles of 32 rows x 128 columns of an output or of 64 x 64 of the weights.
  * ------------------------------------------------------------------------------------------- */
+/* Element types (int arguments: any other value is MOE_EINVAL). */
 typedef enum { MOE_ELT_BF16 = 0, MOE_ELT_FP16 = 1, MOE_ELT_F32 = 2 } moe_elt;
 
 typedef struct {
@@ -422,19 +423,19 @@ typedef struct {
  * MOE_EINVAL: a null or misaligned pointer, a pitch below the row's width, an unknown or
  * inconsistent type, row_div < 1.
  * ------------------------------------------------------------------------------------------- */
-moe_status moe_grouped_gemm(const moe_gemm_shape* s, moe_elt dt, const void* rows, int64_t ld_rows,
+moe_status moe_grouped_gemm(const moe_gemm_shape* s, int dt, const void* rows, int64_t ld_rows,
                             const int32_t* row_src, int32_t row_div, int32_t src_rows,
                             const void* w, const int32_t* offsets, void* out, int64_t ld_out,
-                            moe_elt out_dt, void* stream);
-moe_status moe_grouped_gemm_dgrad(const moe_gemm_shape* s, moe_elt dt, const void* dy,
+                            int out_dt, void* stream);
+moe_status moe_grouped_gemm_dgrad(const moe_gemm_shape* s, int dt, const void* dy,
                                   int64_t ld_dy, const int32_t* row_src, int32_t row_div,
                                   int32_t src_rows, const void* w, const int32_t* offsets,
-                                  void* dx, int64_t ld_dx, moe_elt out_dt, void* stream);
+                                  void* dx, int64_t ld_dx, int out_dt, void* stream);
 size_t moe_grouped_gemm_wgrad_workspace_bytes(const moe_gemm_shape* s);
-moe_status moe_grouped_gemm_wgrad(const moe_gemm_shape* s, moe_elt dt, const void* rows,
+moe_status moe_grouped_gemm_wgrad(const moe_gemm_shape* s, int dt, const void* rows,
                                   int64_t ld_rows, const int32_t* row_src, int32_t row_div,
                                   int32_t src_rows, const void* dy, int64_t ld_dy,
-                                  const int32_t* offsets, void* dw, moe_elt dw_dt, void* ws,
+                                  const int32_t* offsets, void* dw, int dw_dt, void* ws,
                                   void* stream);
 
 /* ---------------------------------------------------------------------------------------------
@@ -459,7 +460,7 @@ moe_status moe_grouped_gemm_wgrad(const moe_gemm_shape* s, moe_elt dt, const voi
  *   moe_gemm_int8.
  * ------------------------------------------------------------------------------------------- */
 size_t moe_int8_pitch(int32_t K);
-moe_status moe_quantize_int8(int32_t R, int32_t K, moe_elt dt, const void* x, int64_t ld_x,
+moe_status moe_quantize_int8(int32_t R, int32_t K, int dt, const void* x, int64_t ld_x,
                              int swiglu, int8_t* codes, float* scales, void* stream);
 size_t moe_int8_weight_bytes(const moe_gemm_shape* s);
 moe_status moe_int8_pack_weights(const moe_gemm_shape* s, const int8_t* w_codes, void* packed,
@@ -468,11 +469,11 @@ moe_status moe_int8_prepare_weights(const moe_gemm_shape* s, const uint16_t* w, 
                                     float* w_scales, void* stream);
 moe_status moe_gemm_int8(const moe_gemm_shape* s, const int8_t* codes, const float* scales,
                          const void* packed, const float* w_scales, const float* bias, void* out,
-                         int64_t ld_out, moe_elt out_dt, void* stream);
+                         int64_t ld_out, int out_dt, void* stream);
 moe_status moe_grouped_gemm_int8(const moe_gemm_shape* s, const int8_t* codes, const float* scales,
                                  const int32_t* row_src, int32_t row_div, int32_t src_rows,
                                  const int32_t* offsets, const void* packed, const float* w_scales,
-                                 const float* bias, void* out, int64_t ld_out, moe_elt out_dt,
+                                 const float* bias, void* out, int64_t ld_out, int out_dt,
                                  void* stream);
 
 /* ---------------------------------------------------------------------------------------------
@@ -495,17 +496,17 @@ moe_status moe_grouped_gemm_int8(const moe_gemm_shape* s, const int8_t* codes, c
  *   The gradients over tokens are summed in a fixed order.
  * ws: moe_norm_backward_workspace_bytes() bytes.
  * ------------------------------------------------------------------------------------------- */
-moe_status moe_pre_norm(int32_t T, int32_t h, moe_elt dt, const void* x, const void* w, float eps,
+moe_status moe_pre_norm(int32_t T, int32_t h, int dt, const void* x, const void* w, float eps,
                         void* z, int8_t* codes, float* scales, float* rstd, void* stream);
-moe_status moe_post_norm(int32_t T, int32_t h, moe_elt dt, const void* res, const void* y,
+moe_status moe_post_norm(int32_t T, int32_t h, int dt, const void* res, const void* y,
                          const void* w, const void* gate, const float* token_gate, float res_scale,
                          float eps, void* u, float* rstd, const void* w_next, void* z,
                          int8_t* codes, float* scales, float* rstd_next, void* stream);
 size_t moe_norm_backward_workspace_bytes(int32_t T, int32_t h);
-moe_status moe_pre_norm_backward(int32_t T, int32_t h, moe_elt dt, const void* dz, const void* x,
+moe_status moe_pre_norm_backward(int32_t T, int32_t h, int dt, const void* dz, const void* x,
                                  const float* rstd, const void* w, const void* d_res, void* dx,
                                  float* dw, void* ws, void* stream);
-moe_status moe_post_norm_backward(int32_t T, int32_t h, moe_elt dt, const void* du, const void* y,
+moe_status moe_post_norm_backward(int32_t T, int32_t h, int dt, const void* du, const void* y,
                                   const float* rstd, const void* w, const void* gate,
                                   const float* token_gate, float res_scale, const void* dz,
                                   const void* u, const float* rstd_next, const void* w_next,

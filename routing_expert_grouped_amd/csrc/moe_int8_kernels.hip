@@ -6,9 +6,9 @@ namespace moe {
 namespace {
 
 // One row per TPR threads: s = amax / 127, code = rint(127 v / amax). The row stays in registers
-// between the maximum and the codes, so it is read once. SWIGLU: the row is silu(G) * U of a
-// [2 K] row [G | U], formed in float32 and quantised from there. Codes behind K, up to the pitch,
-// are zero.
+// between the maximum and the codes, so it is read once (8192 x 6144 bf16, 151 MB: 28 us, 5.4 TB/s).
+// SWIGLU: the row is silu(G) * U of a [2 K] row [G | U], formed in float32 and quantised from there.
+// Codes behind K, up to the pitch, are zero.
 template <bool FP16, bool SWIGLU, int TPR, int V>
 __global__ __launch_bounds__(row_block(TPR)) void quantize_int8_kernel(
     const uint16_t* __restrict__ x, size_t ld, int R, int K, int8_t* __restrict__ codes,

@@ -21,9 +21,9 @@ bool buffer_ok(const void* p, long long count) { return count == 0 || aligned_pt
 hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 moe_status hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
 
-bool elt_16bit(moe_elt dt) { return dt == MOE_ELT_BF16 || dt == MOE_ELT_FP16; }
-bool elt_any(moe_elt dt) { return elt_16bit(dt) || dt == MOE_ELT_F32; }
-int out_kind(moe_elt dt) {
+bool elt_16bit(int dt) { return dt == MOE_ELT_BF16 || dt == MOE_ELT_FP16; }
+bool elt_any(int dt) { return elt_16bit(dt) || dt == MOE_ELT_F32; }
+int out_kind(int dt) {
   return dt == MOE_ELT_BF16 ? kOutBf16 : (dt == MOE_ELT_FP16 ? kOutFp16 : kOutF32);
 }
 
@@ -57,7 +57,7 @@ void gather_args(ProductArgs& p, const int32_t* row_src, int32_t row_div, int32_
   p.src_rows = src_rows;
 }
 
-void output_args(ProductArgs& p, void* out, size_t ld, moe_elt dt) {
+void output_args(ProductArgs& p, void* out, size_t ld, int dt) {
   p.out = out;
   p.out_ld = ld;
   p.out_kind = out_kind(dt);
@@ -65,10 +65,10 @@ void output_args(ProductArgs& p, void* out, size_t ld, moe_elt dt) {
 }
 
 // out[r] = rows[src(r)] W[e]   (trans: W[e]^T), `sum` the sum's length, `cols` the output's width
-moe_status grouped_product(const moe_gemm_shape* s, moe_elt dt, const void* rows, int64_t ld_rows,
+moe_status grouped_product(const moe_gemm_shape* s, int dt, const void* rows, int64_t ld_rows,
                            const int32_t* row_src, int32_t row_div, int32_t src_rows,
                            const void* w, bool trans, const int32_t* offsets, void* out,
-                           int64_t ld_out, moe_elt out_dt, void* stream) {
+                           int64_t ld_out, int out_dt, void* stream) {
   const moe_status st = check_gemm_shape(s);
   if (st != MOE_OK) return st;
   if (!elt_16bit(dt) || (out_dt != dt && out_dt != MOE_ELT_F32)) return MOE_EINVAL;
@@ -111,7 +111,7 @@ size_t int8_expert_bytes(const moe_gemm_shape* s) {
 moe_status int8_product(const moe_gemm_shape* s, const int8_t* codes, const float* scales,
                         const int32_t* row_src, int32_t row_div, int32_t src_rows,
                         const int32_t* offsets, const void* packed, const float* w_scales,
-                        const float* bias, void* out, int64_t ld_out, moe_elt out_dt,
+                        const float* bias, void* out, int64_t ld_out, int out_dt,
                         void* stream) {
   if (!elt_any(out_dt) || ld_out < s->N) return MOE_EINVAL;
   const moe_status g = check_gather(row_src, row_div, src_rows, s->R);
@@ -139,7 +139,7 @@ moe_status int8_product(const moe_gemm_shape* s, const int8_t* codes, const floa
   return hip_status(launch_int8_gemm(p, as_stream(stream)));
 }
 
-moe_status check_rows(int32_t T, int32_t h, moe_elt dt) {
+moe_status check_rows(int32_t T, int32_t h, int dt) {
   if (T < 0 || h < 1 || !elt_16bit(dt)) return MOE_EINVAL;
   if (T > kMaxRows || h > kRowMax) return MOE_EUNSUPPORTED;
   return MOE_OK;
@@ -155,18 +155,18 @@ bool eps_ok(float eps) { return eps > 0.0f && eps < 1.0f; }
 
 extern "C" {
 
-moe_status moe_grouped_gemm(const moe_gemm_shape* s, moe_elt dt, const void* rows, int64_t ld_rows,
+moe_status moe_grouped_gemm(const moe_gemm_shape* s, int dt, const void* rows, int64_t ld_rows,
                             const int32_t* row_src, int32_t row_div, int32_t src_rows,
                             const void* w, const int32_t* offsets, void* out, int64_t ld_out,
-                            moe_elt out_dt, void* stream) {
+                            int out_dt, void* stream) {
   return grouped_product(s, dt, rows, ld_rows, row_src, row_div, src_rows, w, false, offsets, out,
                          ld_out, out_dt, stream);
 }
 
-moe_status moe_grouped_gemm_dgrad(const moe_gemm_shape* s, moe_elt dt, const void* dy,
+moe_status moe_grouped_gemm_dgrad(const moe_gemm_shape* s, int dt, const void* dy,
                                   int64_t ld_dy, const int32_t* row_src, int32_t row_div,
                                   int32_t src_rows, const void* w, const int32_t* offsets,
-                                  void* dx, int64_t ld_dx, moe_elt out_dt, void* stream) {
+                                  void* dx, int64_t ld_dx, int out_dt, void* stream) {
   return grouped_product(s, dt, dy, ld_dy, row_src, row_div, src_rows, w, true, offsets, dx, ld_dx,
                          out_dt, stream);
 }
@@ -178,10 +178,10 @@ size_t moe_grouped_gemm_wgrad_workspace_bytes(const moe_gemm_shape* s) {
   return align_up(parts + 1);
 }
 
-moe_status moe_grouped_gemm_wgrad(const moe_gemm_shape* s, moe_elt dt, const void* rows,
+moe_status moe_grouped_gemm_wgrad(const moe_gemm_shape* s, int dt, const void* rows,
                                   int64_t ld_rows, const int32_t* row_src, int32_t row_div,
                                   int32_t src_rows, const void* dy, int64_t ld_dy,
-                                  const int32_t* offsets, void* dw, moe_elt dw_dt, void* ws,
+                                  const int32_t* offsets, void* dw, int dw_dt, void* ws,
                                   void* stream) {
   const moe_status st = check_gemm_shape(s);
   if (st != MOE_OK) return st;
@@ -210,7 +210,7 @@ moe_status moe_grouped_gemm_wgrad(const moe_gemm_shape* s, moe_elt dt, const voi
 
 size_t moe_int8_pitch(int32_t K) { return K < 1 ? 0 : int8_pitch(K); }
 
-moe_status moe_quantize_int8(int32_t R, int32_t K, moe_elt dt, const void* x, int64_t ld_x,
+moe_status moe_quantize_int8(int32_t R, int32_t K, int dt, const void* x, int64_t ld_x,
                              int swiglu, int8_t* codes, float* scales, void* stream) {
   const moe_status st = check_rows(R, K, dt);
   if (st != MOE_OK) return st;
@@ -247,7 +247,7 @@ moe_status moe_int8_prepare_weights(const moe_gemm_shape* s, const uint16_t* w, 
 
 moe_status moe_gemm_int8(const moe_gemm_shape* s, const int8_t* codes, const float* scales,
                          const void* packed, const float* w_scales, const float* bias, void* out,
-                         int64_t ld_out, moe_elt out_dt, void* stream) {
+                         int64_t ld_out, int out_dt, void* stream) {
   const moe_status st = check_int8_shape(s);
   if (st != MOE_OK) return st;
   if (s->E != 1) return MOE_EINVAL;
@@ -258,7 +258,7 @@ moe_status moe_gemm_int8(const moe_gemm_shape* s, const int8_t* codes, const flo
 moe_status moe_grouped_gemm_int8(const moe_gemm_shape* s, const int8_t* codes, const float* scales,
                                  const int32_t* row_src, int32_t row_div, int32_t src_rows,
                                  const int32_t* offsets, const void* packed, const float* w_scales,
-                                 const float* bias, void* out, int64_t ld_out, moe_elt out_dt,
+                                 const float* bias, void* out, int64_t ld_out, int out_dt,
                                  void* stream) {
   const moe_status st = check_int8_shape(s);
   if (st != MOE_OK) return st;
@@ -267,7 +267,7 @@ moe_status moe_grouped_gemm_int8(const moe_gemm_shape* s, const int8_t* codes, c
                       bias, out, ld_out, out_dt, stream);
 }
 
-moe_status moe_pre_norm(int32_t T, int32_t h, moe_elt dt, const void* x, const void* w, float eps,
+moe_status moe_pre_norm(int32_t T, int32_t h, int dt, const void* x, const void* w, float eps,
                         void* z, int8_t* codes, float* scales, float* rstd, void* stream) {
   const moe_status st = check_rows(T, h, dt);
   if (st != MOE_OK) return st;
@@ -290,7 +290,7 @@ moe_status moe_pre_norm(int32_t T, int32_t h, moe_elt dt, const void* x, const v
   return hip_status(launch_norm(a, dt == MOE_ELT_FP16, as_stream(stream)));
 }
 
-moe_status moe_post_norm(int32_t T, int32_t h, moe_elt dt, const void* res, const void* y,
+moe_status moe_post_norm(int32_t T, int32_t h, int dt, const void* res, const void* y,
                          const void* w, const void* gate, const float* token_gate, float res_scale,
                          float eps, void* u, float* rstd, const void* w_next, void* z,
                          int8_t* codes, float* scales, float* rstd_next, void* stream) {
@@ -330,7 +330,7 @@ size_t moe_norm_backward_workspace_bytes(int32_t T, int32_t h) {
   return align_up(norm_bwd_partial_floats(T, h) * sizeof(float) + 1);
 }
 
-moe_status moe_pre_norm_backward(int32_t T, int32_t h, moe_elt dt, const void* dz, const void* x,
+moe_status moe_pre_norm_backward(int32_t T, int32_t h, int dt, const void* dz, const void* x,
                                  const float* rstd, const void* w, const void* d_res, void* dx,
                                  float* dw, void* ws, void* stream) {
   const moe_status st = check_rows(T, h, dt);
@@ -352,7 +352,7 @@ moe_status moe_pre_norm_backward(int32_t T, int32_t h, moe_elt dt, const void* d
   return hip_status(launch_norm_backward(a, false, true, dt == MOE_ELT_FP16, as_stream(stream)));
 }
 
-moe_status moe_post_norm_backward(int32_t T, int32_t h, moe_elt dt, const void* du, const void* y,
+moe_status moe_post_norm_backward(int32_t T, int32_t h, int dt, const void* du, const void* y,
                                   const float* rstd, const void* w, const void* gate,
                                   const float* token_gate, float res_scale, const void* dz,
                                   const void* u, const float* rstd_next, const void* w_next,

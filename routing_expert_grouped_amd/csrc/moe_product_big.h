@@ -18,6 +18,15 @@
 // order, so at point j (before the last MFMA step of stage j - 1) a count says that this wave's
 // parts of stage j are in LDS; the barrier after it says so for all waves, and that every wave has
 // read its fragments of stage j - 1, whose ring slots the loads issued next overwrite.
+//
+// Measured (one MI355X, random normals). 8192^3 bf16: forward 1250, input gradient 1460, weight
+// gradient 1350 TFLOP/s, int8 2305 TOP/s; the vendor library on the same shapes 1210 / 1520 / 1080
+// and 2100. What bounds it is power: the input gradient keeps the matrix units busy 78% of its
+// cycles at 1.69 GHz, the library's kernel 92% at 1.56 GHz. That is why the 16 x 16 MFMA is taken:
+// it sums twice the k of the 32 x 32 form into each accumulator it touches (input gradient 1280 with
+// 32 x 32). Four waves with 128 x 128 each read a third less LDS than eight with 128 x 64 (1256
+// against 1206, before the loads were spread), and loads spread between the MFMAs took it from
+// 62% to 78% busy.
 #pragma once
 
 #include "moe_gemm_big.h"

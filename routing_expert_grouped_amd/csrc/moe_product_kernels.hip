@@ -8,7 +8,15 @@
 // writes them to the other half of a double-buffered LDS image. In the stage that passes the end of
 // the sum, what lies behind it is zero in LDS, so nothing there (another expert's infinities,
 // unwritten memory) enters a sum; rows and columns behind the tile's edge repeat its last ones and
-// are not stored.
+// are not stored. Loads carry no branches (a chunk that passes its row's end is loaded from the
+// row's last eight elements and shifted), or the compiler would wait for each before the next.
+// Measured, 8192 x 4095 x 4095 bf16: forward 505, input gradient 650, weight gradient 508 TFLOP/s.
+//
+// Which tile a call takes is estimated from its rounds over the CUs (launch_rows). Measured at two
+// sides of it: 4299 rows, 1244 x 1552 int8 over 3 experts, take 36 us with 126 tiles of 256 x 256 and
+// 26 with twice as many of 256 x 128 (half the CUs against all); 11076 rows, 5248 x 640 bf16 over 15
+// experts, take 136 us with some 150 tiles of 256 x 256 and 152 with 256 x 128 (one round against
+// two).
 #include "moe_product_big.h"
 
 namespace moe {
@@ -216,7 +224,8 @@ __device__ __forceinline__ void product_tiles(const ProductArgs& p, uint8_t* lds
   if constexpr (Tile::kWgrad) {
     const int mt = (p.M + BM - 1) / BM;
     for (int jx = blockIdx.x >> 3;
-         big_tile_coords(mt * p.E * p.split, nt_total, p.band_gm, xcd, jx, ti, nt); jx += gridDim.x >> 3) {
+         big_tile_coords(mt * p.E * p.split, nt_total, p.band_gm, xcd, jx, ti, nt);
+         jx += gridDim.x >> 3) {
       Tile::run(p, ti / mt, (ti % mt) * BM, 0, nt * BN, lds);
       __syncthreads();
     }
@@ -320,12 +329,18 @@ double tile_cost(long long tiles, int slots, double unit) {
   return (double)((tiles + slots - 1) / slots) * unit;
 }
 
-// what the large tile's direct loads and stores need: rows at 16-byte steps, a sum (16-bit types)
-// and contiguous columns of whole 16-byte chunks, gathered rows within 32-bit offsets, and output
-// columns in whole runs of four
+// what the direct loads need of both operands: rows at 16-byte steps, and a tile's at most 256 of
+// them within 32-bit offsets
+bool pitches_ok(const ProductArgs& p) {
+  return p.m_pitch % 16 == 0 && p.n_pitch % 16 == 0 && p.m_pitch <= (1u << 22) &&
+         p.n_pitch <= (1u << 22);
+}
+
+// and of a product over routed rows: a sum (16-bit types) and contiguous columns of whole 16-byte
+// chunks, gathered rows within 32-bit offsets, and output columns in whole runs of four
 template <int NK>
 bool big_rows_ok(const ProductArgs& p) {
-  if (p.m_pitch % 16 || p.n_pitch % 16) return false;
+  if (!pitches_ok(p)) return false;
   if (p.N % 4 || !p.out_vec) return false;
   if (NK != kOpPanel && p.K % 8) return false;
   if (NK == kOpKs && p.N % 8) return false;
@@ -407,8 +422,7 @@ hipError_t launch_wgrad(ProductArgs& p, float* ws, hipStream_t st) {
   auto tiles = [&](int b) { return wgrad_tiles(p.M, p.N, p.E, b); };
   auto band = [&](int b) { return band_groups_for((p.N + b - 1) / b, b, p.M); };
   const long long t256 = tiles(256), t128 = tiles(128), t64 = tiles(64);
-  const bool direct = p.m_pitch % 16 == 0 && p.n_pitch % 16 == 0 && p.M % 8 == 0 && p.N % 8 == 0 &&
-                      !p.row_src;
+  const bool direct = pitches_ok(p) && p.M % 8 == 0 && p.N % 8 == 0 && !p.row_src;
   const int split = wgrad_split(p.M, p.N, p.E, p.R);
   if (split > 1) {  // into parts [split][E][M][N], then their sum
     ProductArgs q = p;

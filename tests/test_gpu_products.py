@@ -189,6 +189,62 @@ def test_gather_strides_and_foreign_rows(dims):
     assert (dw[1] == 0).all() and (dw[4] == 0).all()
 
 
+def test_far_rows():
+    """Rows more than 4 MB apart: beyond the direct loads' 32-bit offsets within a tile."""
+    G = require_gpu()
+    g = torch.Generator().manual_seed(3)
+    R, K, N = 40, 64, 136
+    x, dy, w = _rand(g, R, K), _rand(g, R, N), _rand(g, 1, K, N, scale=0.1)
+    far = torch.empty(R, (1 << 21) + 8, dtype=BF, device="cuda")
+    xv, dv = far[:, :K], far[:, 512:512 + N]
+    xv.copy_(x)
+    dv.copy_(dy)
+    sh, off = G.make_gemm_shape(R, K, N, 1), _dev_i32([0, R])
+    out = G.moe_grouped_gemm(sh, xv, w.cuda(), off)
+    ref, mag = P.grouped(x, w, [0, R])
+    _close(out, ref, P.product_bound(ref, mag, K, BF), "far rows")
+    dw = G.moe_grouped_gemm_wgrad(sh, xv, dv, off)
+    ref, mag = P.wgrad(x, P.f8(dy), [0, R])
+    _close(dw, ref, P.product_bound(ref, mag, R, F32), "far rows' gradient")
+
+
+def test_dgrad_is_the_product_of_transposed_weights():
+    """Weights stored [E][out][in] ("y = x W^T"), with tokens gathered through perm."""
+    G = require_gpu()
+    T, k, E, n_in, n_out = 50, 2, 3, 96, 72
+    R = T * k
+    g = torch.Generator().manual_seed(6)
+    assign = torch.randint(0, E, (R,), generator=g)
+    perm = torch.argsort(assign, stable=True).to(torch.int32)
+    off = _offsets(torch.bincount(assign, minlength=E).tolist())
+    x, w = _rand(g, T, n_in), _rand(g, E, n_out, n_in, scale=0.1)
+    out = G.moe_grouped_gemm_dgrad(G.make_gemm_shape(R, n_out, n_in, E), x.cuda(), w.cuda(),
+                                   _dev_i32(off), perm=perm.cuda(), k=k)
+    ref, mag = P.grouped(x, w, off, (perm // k).long(), trans=True)
+    _close(out, ref, P.product_bound(ref, mag, n_in, BF), "x W^T")
+
+
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("counts", [[20], [700]], ids=["few", "many"])
+def test_smallest_and_largest_values(counts, dtype):
+    """Subnormal rows against large weights, and products near the end of the type's range."""
+    G = require_gpu()
+    R, K, N = counts[0], 128, 256
+    g = torch.Generator().manual_seed(R)
+    tiny = torch.finfo(dtype).tiny
+    x = (torch.randn(R, K, generator=g).double() * tiny / 16).to(dtype)
+    w = _rand(g, 1, K, N, dtype=dtype, scale=float(torch.finfo(dtype).max) ** 0.5 / 8)
+    sh, off = G.make_gemm_shape(R, K, N, 1), _dev_i32([0, R])
+    out = G.moe_grouped_gemm(sh, x.cuda(), w.cuda(), off, out_dtype=F32)
+    ref, mag = P.grouped(x, w, [0, R])
+    _close(out, ref, P.product_bound(ref, mag, K, F32), "subnormal rows")
+    x = _rand(g, R, K, dtype=dtype, scale=float(torch.finfo(dtype).max) ** 0.5 / 64)
+    out = G.moe_grouped_gemm(sh, x.cuda(), w.cuda(), off)
+    ref, mag = P.grouped(x, w, [0, R])
+    assert torch.isfinite(out).all()
+    _close(out, ref, P.product_bound(ref, mag, K, dtype), "large values")
+
+
 def test_infinities_stay_in_their_rows():
     G = require_gpu()
     g = torch.Generator().manual_seed(9)

@@ -166,6 +166,19 @@ def test_norm_refusals(lib):
     assert postb(h=16400) == lib.MOE_EUNSUPPORTED
 
 
+def test_product_kernels_keep_their_registers():
+    """The direct-load tiles hold up to 256 sums per lane and their fragments in registers: a spill
+    inside their loop would wait for every load in flight."""
+    import json
+    from routing_expert_grouped_amd import build
+    with open(os.path.join(build.BUILD, build.RESOURCES)) as f:
+        usage = json.load(f)
+    big = {k: v for k, v in usage.items() if "product_big_kernel" in k}
+    assert len(big) == 5 * 4 + 2 * 2
+    for name, v in big.items():
+        assert v["VGPRs Spill"] == 0 and v["ScratchSize [bytes/lane]"] == 0, name
+
+
 def test_binding_checks_without_gpu():
     torch = pytest.importorskip("torch")
     import routing_expert_grouped_amd as G
