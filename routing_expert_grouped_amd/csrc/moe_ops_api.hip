@@ -61,7 +61,6 @@ void output_args(ProductArgs& p, void* out, size_t ld, int dt) {
   p.out = out;
   p.out_ld = ld;
   p.out_kind = out_kind(dt);
-  p.out_vec = ld % 4 == 0;
 }
 
 // out[r] = rows[src(r)] W[e]   (trans: W[e]^T), `sum` the sum's length, `cols` the output's width

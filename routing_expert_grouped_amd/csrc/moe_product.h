@@ -51,7 +51,6 @@ struct ProductArgs {
   void* out;
   size_t out_ld;           // elements between output rows
   int out_kind;            // ProductOut
-  int out_vec;             // runs of four columns may be stored as one vector
   const float* m_scale;    // int8: per source row
   const float* n_scale;    // int8: [E][N]
   const float* bias;       // int8: [E][N] or null
@@ -68,6 +67,8 @@ typedef int i32x4v_t __attribute__((ext_vector_type(4)));
 typedef float f32x4v_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef u32x4_t u32x4_any_t __attribute__((aligned(1)));  // a 16-byte load from any address
+typedef f32x4v_t f32x4_any_t __attribute__((aligned(4)));  // stores to any element
+typedef uint32_t u32x2_any_t __attribute__((ext_vector_type(2), aligned(2)));
 
 template <int EL>
 struct ProductTypes {
@@ -360,11 +361,14 @@ __device__ __forceinline__ uint2 round_fp16x4(f32x4v_t v) {
   return __builtin_bit_cast(uint2, __builtin_convertvector(v, f16x4_t));
 }
 
+// Up to four columns n.. of a row from element `at` on. Rows of odd widths start at any element: the
+// vector stores carry no alignment (a step of 1497 x 1001 x 777, three products: 59 us against 68
+// with a store per element).
 __device__ __forceinline__ void store_run(const ProductArgs& p, size_t at, int n, f32x4v_t v) {
   if (p.out_kind == kOutF32) {
     float* o = reinterpret_cast<float*>(p.out) + at;
-    if (p.out_vec && n + 4 <= p.N) {
-      *reinterpret_cast<f32x4v_t*>(o) = v;
+    if (n + 4 <= p.N) {
+      *reinterpret_cast<f32x4_any_t*>(o) = v;
     } else {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
@@ -373,8 +377,8 @@ __device__ __forceinline__ void store_run(const ProductArgs& p, size_t at, int n
   } else {
     const uint2 b = p.out_kind == kOutBf16 ? round_bf16x4(v) : round_fp16x4(v);
     uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + at;
-    if (p.out_vec && n + 4 <= p.N) {
-      *reinterpret_cast<uint2*>(o) = b;
+    if (n + 4 <= p.N) {
+      *reinterpret_cast<u32x2_any_t*>(o) = u32x2_any_t{b.x, b.y};
     } else {
       const uint16_t e[4] = {(uint16_t)b.x, (uint16_t)(b.x >> 16), (uint16_t)b.y,
                              (uint16_t)(b.y >> 16)};

@@ -464,11 +464,21 @@ struct ProductBig {
               p, min(done.row0 + wm * TM + 16 * j + (lane & 15), done.row_end - 1))];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const size_t c = (size_t)done.e * p.N +
-                           min(done.n0 + wn * TN + 16 * i + 4 * (lane >> 4), p.N - 4);
-          sc[i] = *reinterpret_cast<const f32x4v_t*>(p.n_scale + c);
-          bs[i] = p.bias ? *reinterpret_cast<const f32x4v_t*>(p.bias + c)
-                         : f32x4v_t{0.0f, 0.0f, 0.0f, 0.0f};
+          // four columns' values; behind the last whole four of them one by one
+          const int n = done.n0 + wn * TN + 16 * i + 4 * (lane >> 4);
+          const size_t c = (size_t)done.e * p.N;
+          auto four = [&](const float* f) {
+            f32x4v_t v;
+            if (n + 4 <= p.N) {
+              v = *reinterpret_cast<const f32x4_any_t*>(f + c + n);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) v[q] = f[c + min(n + q, p.N - 1)];
+            }
+            return v;
+          };
+          sc[i] = four(p.n_scale);
+          bs[i] = p.bias ? four(p.bias) : f32x4v_t{0.0f, 0.0f, 0.0f, 0.0f};
         }
 #if defined(__HIP_DEVICE_COMPILE__)
 #pragma unroll
@@ -511,10 +521,14 @@ struct ProductBig {
               if constexpr (EL == kPeI8) v[q] = v[q] * ms[j] * sc[i][q];
             }
             if (EL == kPeI8 && p.bias) v += bs[i];
-            if constexpr (KIND == kOutF32) *reinterpret_cast<f32x4v_t*>(o + 16 * i * ES) = v;
-            else
-              *reinterpret_cast<uint2*>(o + 16 * i * ES) =
-                  KIND == kOutBf16 ? round_bf16x4(v) : round_fp16x4(v);
+            if (!WHOLE) {
+              store_run(p, (size_t)(o - reinterpret_cast<uint8_t*>(p.out)) / ES + 16 * i, n + 16 * i, v);
+            } else if constexpr (KIND == kOutF32) {
+              *reinterpret_cast<f32x4_any_t*>(o + 16 * i * ES) = v;
+            } else {
+              const uint2 b = KIND == kOutBf16 ? round_bf16x4(v) : round_fp16x4(v);
+              *reinterpret_cast<u32x2_any_t*>(o + 16 * i * ES) = u32x2_any_t{b.x, b.y};
+            }
           }
         }
       };

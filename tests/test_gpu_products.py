@@ -208,6 +208,40 @@ def test_far_rows():
     _close(dw, ref, P.product_bound(ref, mag, R, F32), "far rows' gradient")
 
 
+@pytest.mark.parametrize("odt", [BF, HF, F32], ids=["bf16", "fp16", "f32"])
+@pytest.mark.parametrize("case", [(700, 517, [300, 0, 400]), (8192, 1003, [8192]),
+                                  (8200, 1799, [8, 8192]), (60, 131, [20, 0, 40])], ids=str)
+def test_odd_output_widths(case, odt):
+    """Outputs whose rows start at any element, and whose width is no whole run of four, at every tile
+    of the direct loads, into a slice of a wider tensor whose other columns keep their values."""
+    G = require_gpu()
+    R, cols, counts = case
+    sums, E, off = 72, len(counts), _offsets(counts)
+    dt = BF if odt == F32 else odt
+    g = torch.Generator().manual_seed(cols)
+    dy, w = _rand(g, R, sums, dtype=dt), _rand(g, E, cols, sums, dtype=dt, scale=0.1)
+    wide = torch.full((R, cols + 10), 7.0, dtype=odt, device="cuda")
+    out = wide[:, :cols]
+    note(f"odd widths {case} {odt}")
+    G.moe_grouped_gemm_dgrad(G.make_gemm_shape(R, cols, sums, E), dy.cuda(), w.cuda(),
+                             _dev_i32(off), out=out)
+    ref, mag = P.grouped(dy, w, off, trans=True)
+    _close(out, ref, P.product_bound(ref, mag, sums, odt), "input gradient")
+    assert (wide[:, cols:] == 7).all()
+
+    q = torch.randint(-127, 128, (E, cols, sums), generator=g, dtype=torch.int8)
+    ws, bias = torch.rand(E, cols, generator=g) / sums, torch.randn(E, cols, generator=g)
+    sh = G.make_gemm_shape(R, sums, cols, E)
+    packed = G.moe_int8_pack_weights(sh, q.cuda())
+    codes, scales = G.moe_quantize_int8(dy.cuda())
+    wide.fill_(7.0)
+    G.moe_grouped_gemm_int8(sh, codes, scales, packed, ws.cuda(), _dev_i32(off), bias=bias.cuda(),
+                            out=out)
+    ref, mag = _int8_ref(codes, scales, q, ws, bias, off, torch.arange(R))
+    _close(out, ref, P.half_step(odt, ref) * (1 + 2.0 ** -8) + 4 * P.EPS24 * mag, "int8")
+    assert (wide[:, cols:] == 7).all()
+
+
 def test_dgrad_is_the_product_of_transposed_weights():
     """Weights stored [E][out][in] ("y = x W^T"), with tokens gathered through perm."""
     G = require_gpu()
