@@ -8,17 +8,17 @@
 // LDS is exact in any order. Splitting over waves instead of columns keeps 256 workgroups busy on a
 // 4096-column product of one token, where a tile of 128 columns would fill 32 CUs.
 //
-// Measured, 7168 x 4096 (29.4 MB of weights from memory), this kernel against the 128-column tile:
-// 1 row 10.1 / 49.6 us, 16 rows 12.8 / 49.7, 64 rows 22 / 58, 128 rows 37 / 57, 256 rows 66 / 57.
+// Measured, 7168 x 4096 (29.4 MB of weights from memory): 1 row 10.1 us (2.9 TB/s), 16 rows 12.7,
+// 32 rows 16.0 (the tiles: 21.7, 22.9, 24.7).
 #include "moe_product.h"
 
 namespace moe {
 namespace {
 
 constexpr int kFewWaves = 8;
-// UNROLL blocks of a wave are in flight at once, as many as its registers hold beside the sums
-template <int NJ, int kFewUnroll>
-__global__ __launch_bounds__(64 * kFewWaves, NJ <= 2 ? 4 : 2) void int8_few_kernel(ProductArgs p) {
+constexpr int kFewUnroll = 4;  // blocks of a wave that are in flight at once
+template <int NJ>
+__global__ __launch_bounds__(64 * kFewWaves, 4) void int8_few_kernel(ProductArgs p) {
   __shared__ i32x4v_t part[kFewWaves][NJ][64];
   __shared__ int scratch[kFewWaves];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -97,16 +97,14 @@ __global__ __launch_bounds__(64 * kFewWaves, NJ <= 2 ? 4 : 2) void int8_few_kern
 }  // namespace
 
 hipError_t launch_int8_few(ProductArgs p, int rows, hipStream_t st) {
-  const int bm = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  const int bm = rows <= 16 ? 16 : 32;
   const int panels = (p.N + 15) / 16;
   const long long tiles = ((long long)(p.R / bm) + (p.E < p.R ? p.E : p.R)) * panels;
   const unsigned grid = (unsigned)((tiles < 512 ? tiles : 512) + 7) / 8 * 8;
   p.band_gm = 1;
   const dim3 g(grid), b(64 * kFewWaves);
-  if (bm == 16) hipLaunchKernelGGL((int8_few_kernel<1, 4>), g, b, 0, st, p);
-  else if (bm == 32) hipLaunchKernelGGL((int8_few_kernel<2, 4>), g, b, 0, st, p);
-  else if (bm == 64) hipLaunchKernelGGL((int8_few_kernel<4, 2>), g, b, 0, st, p);
-  else hipLaunchKernelGGL((int8_few_kernel<8, 2>), g, b, 0, st, p);
+  if (bm == 16) hipLaunchKernelGGL(int8_few_kernel<1>, g, b, 0, st, p);
+  else hipLaunchKernelGGL(int8_few_kernel<2>, g, b, 0, st, p);
   return hipGetLastError();
 }
 

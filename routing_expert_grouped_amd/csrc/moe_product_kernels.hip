@@ -348,15 +348,19 @@ bool big_rows_ok(const ProductArgs& p) {
 
 // The tile of a product over routed rows: the one whose rounds over the CUs are estimated cheapest
 // (a large tile has the higher rate, a small one fills the CUs and wastes less at an expert's
-// end), and 32 rows where an expert has at most 32 on average: reading the weights is all there
-// is, and the smallest tile has the most loads in flight for them.
+// end), and 32 rows of 128 columns where an expert has at most 32 on average: reading the weights is
+// all there is, and this tile has the most loads in flight for them. Unless there are so few of
+// those that most CUs would idle: then 64 x 64 (bf16, 16 rows each, us: 32 tiles, 7168 x 4096, 48
+// against 37; 128 tiles, 8 experts of 4096 x 2048, 25 against 24; 256 tiles, 16 of them, 43
+// against 47).
 template <int EL, int NK>
 hipError_t launch_rows(ProductArgs& p, hipStream_t st) {
   const long long rpe = (p.R + p.E - 1) / p.E;
   const int n256 = (p.N + 255) / 256, n128 = (p.N + 127) / 128, n64 = (p.N + 63) / 64;
   const double c64 = tile_cost(likely_row_tiles(p, 64) * n64, 512, 0.25);
   const bool direct = big_rows_ok<NK>(p);
-  if (rpe <= 32) {
+  const long long hit = p.E < p.R ? p.E : p.R;
+  if (rpe <= 32 && !(direct && hit * n128 <= 128)) {
     const long long tiles = row_tiles(p, 32) * n128;
     p.band_gm = band_groups_for(n128, 32, rpe);
     if (direct) return launch_big<EL, NK, kOpKc, 128, 32, 4, 1, 4, 4, 2>(p, tiles, st);
@@ -478,15 +482,14 @@ hipError_t launch_grouped_wgrad(ProductArgs p, int el, float* ws, hipStream_t st
 }
 
 hipError_t launch_int8_gemm(ProductArgs p, hipStream_t st) {
-  // Too few 128-column tiles to fill the CUs: split the sum over waves instead. The few-row kernel
-  // reads the codes once per 16 columns, so its work grows with rows x columns: measured equal at
-  // rows (each expert's at least 16) x 128-column tiles = 4096 (1 x 128 rows of 7168 x 4096: 37 us
-  // against the tile's 57; 4 x 64 rows: 66 against 49; 8 x 1: 42 against 42), and for short sums,
-  // where a tile's latency is short too, earlier (64 x 2 rows of 512 x 512: 13.5 against 6.4).
-  const long long hit = p.E < p.R ? p.E : p.R, r16 = p.R > 16 * hit ? p.R : 16 * hit;
-  const long long size = r16 * ((p.N + 127) / 128);
-  if (size <= (p.K >= 2048 ? 4096 : 1024))
-    return launch_int8_few(p, (p.R + p.E - 1) / p.E, st);
+  // Few rows and too few tiles of 128 columns to fill the CUs: split the sum over waves instead.
+  // Measured against the tiles, us. 32 tiles: 1 row of 7168 x 4096 10.1 / 17.8, 32 rows 16.0 / 18.6,
+  // of 512 x 512 4.9 / 5.2. 64 tiles: 16 rows of 7168 x 8192 20.3 / 22.3, 32 rows 26.5 / 22.8, 16
+  // rows of 2048 x 8192 8.3 / 7.5.
+  const long long tiles = (long long)(p.E < p.R ? p.E : p.R) * ((p.N + 127) / 128);
+  const int rpe = (p.R + p.E - 1) / p.E;
+  if ((rpe <= 32 && tiles <= 32) || (p.R <= 16 && tiles <= 64 && p.K >= 4096))
+    return launch_int8_few(p, rpe, st);
   return launch_rows<kPeI8, kOpPanel>(p, st);
 }
 
