@@ -3,7 +3,8 @@
 //
 // Two families of tiles. ProductBig (moe_product_big.h) brings its operands to LDS by direct loads
 // and takes what those can address; ProductTile below takes everything else: row pitches that are no
-// multiple of 16 bytes, sums and widths that are no whole chunks, gathered weight gradients. A
+// multiple of 16 bytes, sums (or columns of a strided operand) that are no whole chunks, gathered
+// weight gradients. A
 // thread loads its 16-byte chunks of the stages ahead into registers while the MFMAs run, and
 // writes them to the other half of a double-buffered LDS image. In the stage that passes the end of
 // the sum, what lies behind it is zero in LDS, so nothing there (another expert's infinities,
